@@ -232,6 +232,82 @@ MLA_API mla_status mla_decode_attention_noalloc(const mla_dims* dims, const void
                                                 void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Row operators and the 8-bit projection: the parts of an MLA layer around steps 1 to 5.  The
+ * pages name the 8-bit blocks (hdu-wiki.cn section 5 and Q4: FP8 with one scale per tile or
+ * block) and the decoupled RoPE key; the norm is the usual root-mean-square one.
+ *
+ * 8-bit rows, as written by mla_norm_rows and mla_quantize_rows and read by mla_project_fp8:
+ *   codes  [n_tok, width] uint8 E4M3 codes, codes_ld bytes between rows;
+ *   scales [n_tok, ceil(width / 128)] fp32, dense, one per 128 values of a row (the last block may
+ *          be shorter);  value = code * scale.
+ *   s = amax / 448 and code = e4m3(x * (448 / amax)), each step rounded to fp32 and the code to
+ *   nearest even, as the FP8 cache does; s = 1 for an all-zero block, and a block whose amax is
+ *   below 2^-100 is coded against 2^-100.  A block that holds a NaN or an infinity stands for
+ *   NaN.
+ * Further conventions of these calls:
+ *   - *_ld is the distance between consecutive rows in elements (bytes for codes), at least the
+ *     row's width; elements between the width and *_ld are neither read nor written.
+ *   - act_dtype is the element type of the unquantised rows: MLA_F32 or MLA_BF16.
+ *   - Any width, alignment and *_ld is taken.  16-byte aligned rows (8-byte codes) whose width is
+ *     a multiple of 8 take the faster, vectorised kernels.
+ *   - They are launched with programmatic stream serialization like the projections above, but
+ *     read and write nothing (L2 prefetches apart) before the preceding kernel has completed, so
+ *     any of their inputs may be the output of the preceding call.
+ *   - No workspace, nothing kept between calls: calls on different streams and captured graphs
+ *     do not share anything but the device error word. */
+
+/* mla_norm_rows — root-mean-square norm with the residual's addition and an 8-bit output.
+ *   r = x + residual,  y = r / sqrt(mean(r^2) + eps) * gamma
+ * in fp32 from the unrounded sum r; each output is rounded once.
+ *   x:        [n_tok, width] act;  residual: [n_tok, width] act, or NULL (r = x)
+ *   gamma:    [width] act, or NULL (a weight of 1)
+ *   sum_out:  [n_tok, width] act, r rounded (the next residual), or NULL
+ *   y:        [n_tok, width] act, or NULL;   codes, scales: y as 8-bit rows, or both NULL
+ * At least one output is given.  sum_out may be x or residual, and y may be x (the same pointer
+ * and ld); other overlaps are not allowed.  n_tok == 0 is a no-op. */
+MLA_API mla_status mla_norm_rows(int32_t act_dtype, const void* x, int64_t x_ld, const void* residual,
+                         int64_t residual_ld, const void* gamma, int32_t n_tok, int32_t width,
+                         float eps, void* sum_out, int64_t sum_ld, void* y, int64_t y_ld,
+                         uint8_t* codes, int64_t codes_ld, float* scales, void* stream);
+
+/* mla_quantize_rows — rows as 8-bit rows, without a norm (the attention output in front of an
+ * 8-bit output projection).  x: [n_tok, width] act.  n_tok == 0 is a no-op. */
+MLA_API mla_status mla_quantize_rows(int32_t act_dtype, const void* x, int64_t x_ld, int32_t n_tok,
+                             int32_t width, uint8_t* codes, int64_t codes_ld, float* scales,
+                             void* stream);
+
+/* mla_project_fp8 — 8-bit projection with block scales.
+ *   out[t, n] = sum_b x_scales[t, b] w_scales[n / 128, b] sum_{k in block b} x[t, k] w[n, k]
+ * over the 128-value blocks b of the width; the sum within a block and the scaled sum over blocks
+ * are fp32, and the result is rounded once to act_dtype.
+ *   x_codes:  [n_tok, width] 8-bit rows with x_scales [n_tok, ceil(width / 128)]
+ *   w_codes:  [n_out, width] uint8 E4M3 codes, dense
+ *   w_scales: [ceil(n_out / 128), ceil(width / 128)] fp32, one per 128 x 128 block
+ *   out:      [n_tok, n_out] act_dtype, out_ld elements between rows
+ * The result does not depend on timing.  Rows of x and w on 16-byte boundaries (pointers, x_ld and
+ * width) take the tensor-core kernels; other layouts the general one.  n_tok == 0 is a no-op. */
+MLA_API mla_status mla_project_fp8(int32_t act_dtype, const uint8_t* x_codes, int64_t x_ld,
+                           const float* x_scales, int32_t n_tok, const uint8_t* w_codes,
+                           const float* w_scales, int32_t n_out, int32_t width, void* out,
+                           int64_t out_ld, void* stream);
+
+/* mla_append_rows — append rows that are already projected: step 1 without its products, for
+ * callers whose down projection is another kernel (mla_project_fp8, say).
+ *   c = kv[t, :d_c], k = kv[t, d_c : d_c + d_rope]; with gamma, c is normed as in mla_norm_rows
+ *   (over its d_c values); k is rotated by RoPE at pos[t]; the row is stored as in
+ *   mla_append_cache (F32 / BF16 row, or E4M3 codes and scales plus the bf16 rope row).
+ *   kv:       [n_tok, d_c + d_rope] act, kv_ld elements between rows
+ *   gamma:    [d_c] act, or NULL: the latent is stored as it is and eps is not used
+ *   seq_idx, pos, rope_cos, rope_sin, rope_rows, cache: as in mla_append_cache, and so are the
+ *   handling of bad sequence numbers, positions and page ids (the token is skipped and reported)
+ *   and of two tokens with the same (sequence, position).  n_tok == 0 is a no-op.
+ * Of dims the call uses d_c, d_rope, page_size, act_dtype and cache_dtype. */
+MLA_API mla_status mla_append_rows(const mla_dims* dims, const void* kv, int64_t kv_ld, int32_t n_tok,
+                           const int32_t* seq_idx, const int32_t* pos, const void* gamma, float eps,
+                           const float* rope_cos, const float* rope_sin, int32_t rope_rows,
+                           const mla_cache* cache, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * Status helpers. */
 MLA_API const char* mla_status_string(mla_status s);
 /* Synchronises `stream`, then reads and clears the current device's error word.

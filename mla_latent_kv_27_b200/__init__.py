@@ -14,7 +14,7 @@ _BINDING_NAMES = {
     "mla_decode_workspace_size", "mla_decode_attention", "mla_output_up", "mla_status_string",
     "mla_check_device_error", "mla_version", "mla_launch_count", "mla_dims", "mla_cache", "MlaError", "lib_handle",
     "MLA_F32", "MLA_BF16", "MLA_FP8_E4M3", "EXPORTED", "mla_decode_attention_noalloc",
-    "MLA_NOALLOC_SCRATCH_BYTES",
+    "MLA_NOALLOC_SCRATCH_BYTES", "mla_norm_rows", "mla_quantize_rows", "mla_project_fp8", "mla_append_rows",
 }
 
 

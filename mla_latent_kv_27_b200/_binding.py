@@ -21,6 +21,7 @@ EXPORTED = (
     "mla_rope_table", "mla_append_workspace_size", "mla_append_cache", "mla_absorb_query",
     "mla_decode_workspace_size", "mla_decode_attention", "mla_output_up", "mla_status_string",
     "mla_check_device_error", "mla_version", "mla_launch_count", "mla_decode_attention_noalloc",
+    "mla_norm_rows", "mla_quantize_rows", "mla_project_fp8", "mla_append_rows",
 )
 
 MLA_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -51,6 +52,7 @@ def _load():
                           "(the library has no fallback)")
     lib = ctypes.CDLL(os.fspath(_LIB_PATH))
     P, I32, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
+    I64 = ctypes.c_int64
     D, C = ctypes.POINTER(mla_dims), ctypes.POINTER(mla_cache)
     sig = {
         "mla_rope_table": (I32, [I32, I32, F32, P, P, P]),
@@ -61,6 +63,10 @@ def _load():
         "mla_decode_attention": (I32, [D, P, C, P, I32, I32, I32, I32, P, SZ, P, P, P]),
         "mla_output_up": (I32, [D, P, I32, P, P, P]),
         "mla_decode_attention_noalloc": (I32, [D, P, C, P, I32, I32, I32, I32, P, P, P]),
+        "mla_norm_rows": (I32, [I32, P, I64, P, I64, P, I32, I32, F32, P, I64, P, I64, P, I64, P, P]),
+        "mla_quantize_rows": (I32, [I32, P, I64, I32, I32, P, I64, P, P]),
+        "mla_project_fp8": (I32, [I32, P, I64, P, I32, P, P, I32, I32, P, I64, P]),
+        "mla_append_rows": (I32, [D, P, I64, I32, P, P, P, F32, P, P, I32, C, P]),
         "mla_status_string": (ctypes.c_char_p, [I32]),
         "mla_check_device_error": (I32, [P, ctypes.POINTER(I32)]),
         "mla_version": (I32, []),
@@ -162,6 +168,32 @@ def mla_decode_attention_noalloc(dims, q_packed, cache: mla_cache, seq_lens, bat
 def mla_output_up(dims, o_lat, n_tok, w_uv, out, stream=None):
     _check(_lib.mla_output_up(ctypes.byref(dims), _p(o_lat), n_tok, _p(w_uv), _p(out), _s(stream)),
            "mla_output_up")
+
+
+def mla_norm_rows(act_dtype, x, x_ld, residual, residual_ld, gamma, n_tok, width, eps, sum_out, sum_ld, y,
+                  y_ld, codes, codes_ld, scales, stream=None):
+    _check(_lib.mla_norm_rows(act_dtype, _p(x), x_ld, _p(residual), residual_ld, _p(gamma), n_tok, width,
+                              eps, _p(sum_out), sum_ld, _p(y), y_ld, _p(codes), codes_ld, _p(scales),
+                              _s(stream)), "mla_norm_rows")
+
+
+def mla_quantize_rows(act_dtype, x, x_ld, n_tok, width, codes, codes_ld, scales, stream=None):
+    _check(_lib.mla_quantize_rows(act_dtype, _p(x), x_ld, n_tok, width, _p(codes), codes_ld, _p(scales),
+                                  _s(stream)), "mla_quantize_rows")
+
+
+def mla_project_fp8(act_dtype, x_codes, x_ld, x_scales, n_tok, w_codes, w_scales, n_out, width, out,
+                    out_ld, stream=None):
+    _check(_lib.mla_project_fp8(act_dtype, _p(x_codes), x_ld, _p(x_scales), n_tok, _p(w_codes),
+                                _p(w_scales), n_out, width, _p(out), out_ld, _s(stream)),
+           "mla_project_fp8")
+
+
+def mla_append_rows(dims, kv, kv_ld, n_tok, seq_idx, pos, gamma, eps, rope_cos, rope_sin, rope_rows,
+                    cache: mla_cache, stream=None):
+    _check(_lib.mla_append_rows(ctypes.byref(dims), _p(kv), kv_ld, n_tok, _p(seq_idx), _p(pos), _p(gamma),
+                                eps, _p(rope_cos), _p(rope_sin), rope_rows, ctypes.byref(cache),
+                                _s(stream)), "mla_append_rows")
 
 
 def mla_check_device_error(stream=None):

@@ -8,6 +8,8 @@
 
 #include "mla_internal.cuh"
 #include "decode_tc.cuh"
+#include "proj_fp8.cuh"
+#include "rows.cuh"
 
 namespace mla {
 
@@ -101,6 +103,12 @@ static int simt_auto_split(const mla_dims* d, int batch, int s_q, int max_pages)
 static int effective_split(const mla_dims* d, int batch, int s_q, int n_split, int max_pages) {
   if (n_split > 0) return n_split;
   return simt_auto_split(d, batch, s_q, max_pages);
+}
+
+// An element type of the row operators and projections that take no mla_dims.
+static mla_status check_act(int32_t act) {
+  if (!dtype_ok(act)) return MLA_ERR_INVALID_ARG;
+  return act == MLA_FP8_E4M3 ? MLA_ERR_UNSUPPORTED : MLA_OK;
 }
 
 // The two partitioned kernels: the small-head one (at most 16 heads, bf16) and the tcgen05 one.
@@ -279,6 +287,72 @@ mla_status mla_output_up(const mla_dims* dims, const void* o_lat, int32_t n_tok,
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
   return cuda_status(launch_output_up(*dims, o_lat, n_tok, w_uv, out, err, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status mla_norm_rows(int32_t act_dtype, const void* x, int64_t x_ld, const void* residual,
+                         int64_t residual_ld, const void* gamma, int32_t n_tok, int32_t width,
+                         float eps, void* sum_out, int64_t sum_ld, void* y, int64_t y_ld,
+                         uint8_t* codes, int64_t codes_ld, float* scales, void* stream) {
+  mla_status s = check_act(act_dtype);
+  if (s != MLA_OK) return s;
+  if (n_tok < 0 || width <= 0 || !(eps >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return MLA_OK;
+  if (!x || (!sum_out && !y && !codes) || (codes == nullptr) != (scales == nullptr))
+    return MLA_ERR_INVALID_ARG;
+  if (x_ld < width || (residual && residual_ld < width) || (sum_out && sum_ld < width) ||
+      (y && y_ld < width) || (codes && codes_ld < width))
+    return MLA_ERR_INVALID_ARG;
+  const RowsArgs a = {act_dtype, x, x_ld, residual, residual_ld, gamma, n_tok, width, eps,
+                      sum_out, sum_ld, y, y_ld, codes, codes_ld, scales};
+  return cuda_status(launch_rows(a, true, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status mla_quantize_rows(int32_t act_dtype, const void* x, int64_t x_ld, int32_t n_tok,
+                             int32_t width, uint8_t* codes, int64_t codes_ld, float* scales,
+                             void* stream) {
+  mla_status s = check_act(act_dtype);
+  if (s != MLA_OK) return s;
+  if (n_tok < 0 || width <= 0) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return MLA_OK;
+  if (!x || !codes || !scales || x_ld < width || codes_ld < width) return MLA_ERR_INVALID_ARG;
+  const RowsArgs a = {act_dtype, x, x_ld, nullptr, 0, nullptr, n_tok, width, 0.f,
+                      nullptr, 0, nullptr, 0, codes, codes_ld, scales};
+  return cuda_status(launch_rows(a, false, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status mla_project_fp8(int32_t act_dtype, const uint8_t* x_codes, int64_t x_ld,
+                           const float* x_scales, int32_t n_tok, const uint8_t* w_codes,
+                           const float* w_scales, int32_t n_out, int32_t width, void* out,
+                           int64_t out_ld, void* stream) {
+  mla_status s = check_act(act_dtype);
+  if (s != MLA_OK) return s;
+  if (n_tok < 0 || n_out <= 0 || width <= 0) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return MLA_OK;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !out || x_ld < width || out_ld < n_out)
+    return MLA_ERR_INVALID_ARG;
+  int* err = error_word_ptr();
+  if (!err) return MLA_ERR_CUDA;
+  const Fp8Args a = {act_dtype, x_codes, x_ld, x_scales, w_codes, w_scales, n_tok, n_out, width,
+                     out, out_ld, err};
+  return cuda_status(launch_project_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status mla_append_rows(const mla_dims* dims, const void* kv, int64_t kv_ld, int32_t n_tok,
+                           const int32_t* seq_idx, const int32_t* pos, const void* gamma, float eps,
+                           const float* rope_cos, const float* rope_sin, int32_t rope_rows,
+                           const mla_cache* cache, void* stream) {
+  mla_status s = check_dims(dims);
+  if (s != MLA_OK) return s;
+  if (n_tok < 0 || !(eps >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return MLA_OK;
+  if ((s = check_cache(dims, cache)) != MLA_OK) return s;
+  if (!kv || !seq_idx || !pos || !rope_cos || !rope_sin || rope_rows <= 0) return MLA_ERR_INVALID_ARG;
+  if (kv_ld < (int64_t)dims->d_c + dims->d_rope) return MLA_ERR_INVALID_ARG;
+  int* err = error_word_ptr();
+  if (!err) return MLA_ERR_CUDA;
+  return cuda_status(launch_append_rows(*dims, kv, kv_ld, n_tok, seq_idx, pos, gamma, eps, rope_cos,
+                                        rope_sin, rope_rows, make_view(dims, cache), err,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,390 @@
+"""GPU parity of the row operators (norm, quantisation, append of projected rows) with plain fp64
+formulas on the same inputs.
+
+Tolerances.  U = 2^-24 is half a step of fp32.  The mean of squares is a sum of positive terms: a
+value passes through at most ceil(width / 256) + 20 additions (one thread's values, then the
+tree), so its relative error is below (ceil(width / 256) + 21) U, half of that after the root; the
+root, two products and the residual's sum add a few U more.  At the widths used here (up to 33000)
+that is under 80 U: REL = 128 U = 2^-17.  Storing rounds once: half a step of the output type,
+2^-8 (bf16) or U (fp32) relative.  An E4M3 code is off by half a step of the code: 2^-4 of the
+value, or 2^-10 scales where the code is subnormal (step 2^-9); a decision that falls the other
+way because of REL costs REL more.
+"""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from mla_latent_kv_27_b200 import workloads as wl
+from oracle import mla_oracle as orc
+
+pytestmark = pytest.mark.gpu
+
+REL = 2.0 ** -17
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+ACT = [torch.bfloat16, torch.float32]
+GUARD = 77.0
+
+
+def dt(lib, t):
+    return lib.MLA_BF16 if t == torch.bfloat16 else lib.MLA_F32
+
+
+def randn(shape, seed, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda") * scale
+
+
+def decoded(codes, scales, width):
+    v = codes[:, :width].contiguous().view(torch.float8_e4m3fn).double()
+    return v * scales.double().repeat_interleave(128, 1)[:, :width]
+
+
+def check_codes(codes, scales, y, width, rel=REL):
+    """8-bit rows against the exact values y [T, width] (fp64)."""
+    assert torch.isfinite(scales).all()
+    kb = -(-width // 128)
+    pad = torch.nn.functional.pad(y, (0, kb * 128 - width)).view(y.shape[0], kb, 128)
+    amax = pad.abs().amax(-1)
+    want = torch.where(amax == 0, torch.ones_like(amax), amax.clamp(min=2.0 ** -100) / 448)
+    assert ((scales.double() - want).abs() <= (rel + 2.0 ** -24) * want).all()
+    s = scales.double().repeat_interleave(128, 1)[:, :width]
+    err = (decoded(codes, scales, width) - y).abs()
+    assert (err <= 2.0 ** -4 * y.abs() * (1 + 2 * rel) + 2.0 ** -10 * s + 2 * rel * y.abs()).all()
+
+
+def near(got, want, extra=REL):
+    tol = (HALF[got.dtype] + extra) * want.abs()
+    assert ((got.double() - want).abs() <= tol).all(), float(((got.double() - want).abs() - tol).max())
+
+
+def norm_ref(x, res, gamma, eps):
+    r = x.double() if res is None else x.double() + res.double()
+    y = r / torch.sqrt((r * r).mean(-1, keepdim=True) + eps)
+    return r, y if gamma is None else y * gamma.double()
+
+
+def strided(t, width, ld, act):
+    return torch.full((t, ld), GUARD, dtype=act, device="cuda")
+
+
+def run_norm(lib, act, t, width, *, res=True, gamma=True, outs=("sum", "y", "q"), pad=0, offset=0, seed=0, eps=1e-6,
+             x=None):
+    ld = width + pad
+    cut = lambda m: m.reshape(-1)[offset:offset + t * ld].view(t, ld) if offset else m  # noqa: E731
+    buf = torch.full((t * ld + offset,), GUARD, dtype=act, device="cuda")
+    X = cut(buf) if offset else buf.view(t, ld)
+    X[:, :width] = (randn((t, width), seed) if x is None else x).to(act)
+    R = G = None
+    if res:
+        R = strided(t, width, ld, act)
+        R[:, :width] = randn((t, width), seed + 1, 2.0).to(act)
+    if gamma:
+        G = (1 + 0.2 * randn((width,), seed + 2)).to(act)
+    S = strided(t, width, ld, act) if "sum" in outs else None
+    Y = strided(t, width, ld, act) if "y" in outs else None
+    Q = torch.full((t, ld), 99, dtype=torch.uint8, device="cuda") if "q" in outs else None
+    SC = torch.full((t, -(-width // 128)), float("nan"), device="cuda") if "q" in outs else None
+    lib.mla_norm_rows(dt(lib, act), X, ld, R, ld, G, t, width, eps, S, ld, Y, ld, Q, ld, SC)
+    torch.cuda.synchronize()
+    assert lib.mla_check_device_error()[0] == 0
+    r, y = norm_ref(X[:, :width], None if R is None else R[:, :width], G, eps)
+    if S is not None:
+        near(S[:, :width], r, 2.0 ** -24)
+        assert (S[:, width:] == GUARD).all()
+    if Y is not None:
+        near(Y[:, :width], y)
+        assert (Y[:, width:] == GUARD).all()
+    if Q is not None:
+        check_codes(Q, SC, y, width)
+        assert (Q[:, width:] == 99).all()
+
+
+# widths around the 8-value chunk, the 128-value block and the launch shapes (256, 1024, 4096 chunks)
+WIDTHS = [1, 7, 8, 100, 127, 128, 136, 512, 1000, 1536, 2048, 2056, 7168, 8192, 8200, 16384, 32768, 33000]
+
+
+@pytest.mark.parametrize("act", ACT)
+@pytest.mark.parametrize("width", WIDTHS)
+def test_norm_widths(lib, act, width):
+    run_norm(lib, act, 3, width, seed=width)
+
+
+@pytest.mark.parametrize("act", ACT)
+@pytest.mark.parametrize("t", [1, 2, 65, 1500])
+def test_norm_rows_count(lib, act, t):
+    run_norm(lib, act, t, 1536, seed=t)
+
+
+@pytest.mark.parametrize("pad,offset", [(8, 0), (1, 0), (0, 1), (24, 8)])
+def test_norm_strides_and_alignment(lib, pad, offset):
+    for act in ACT:
+        run_norm(lib, act, 5, 640, pad=pad, offset=offset)
+
+
+@pytest.mark.parametrize("res", [True, False])
+@pytest.mark.parametrize("gamma", [True, False])
+@pytest.mark.parametrize("outs", [("sum",), ("y",), ("q",), ("sum", "q")])
+def test_norm_optional_arguments(lib, res, gamma, outs):
+    for width in (520, 515):
+        run_norm(lib, torch.bfloat16, 4, width, res=res, gamma=gamma, outs=outs)
+
+
+@pytest.mark.parametrize("width", [1024, 1001])
+def test_norm_in_place(lib, width):
+    """sum_out over the residual and y over x."""
+    t = 6
+    x, res = randn((t, width), 1).bfloat16(), randn((t, width), 2).bfloat16()
+    g = (1 + 0.1 * randn((width,), 3)).bfloat16()
+    r, y = norm_ref(x, res, g, 1e-5)
+    lib.mla_norm_rows(lib.MLA_BF16, x, width, res, width, g, t, width, 1e-5, res, width, x, width, None, 0, None)
+    torch.cuda.synchronize()
+    near(res, r, 2.0 ** -24)
+    near(x, y)
+
+
+@pytest.mark.parametrize("width", [384, 385])
+def test_norm_zero_rows(lib, width):
+    """An all-zero row: y = 0, codes 0, scales 1; rows beside it are untouched by it."""
+    x = randn((4, width), 5)
+    x[2] = 0
+    run_norm(lib, torch.float32, 4, width, res=False, x=x)
+    q = torch.empty((4, width), dtype=torch.uint8, device="cuda")
+    s = torch.empty((4, -(-width // 128)), device="cuda")
+    lib.mla_quantize_rows(lib.MLA_F32, x, width, 4, width, q, width, s)
+    torch.cuda.synchronize()
+    assert (q[2] == 0).all() and (s[2] == 1).all()
+
+
+@pytest.mark.parametrize("act", ACT)
+@pytest.mark.parametrize("width", [8, 100, 128, 1000, 2048, 2304, 16384, 40000])
+def test_quantize_equals_the_fp32_decision(lib, act, width):
+    """Same inputs, same fp32 steps: codes and scales are the oracle's, bit for bit."""
+    t = 7
+    x = (randn((t, width), width) * torch.exp(randn((t, 1), 9))).to(act)
+    q = torch.full((t, width), 99, dtype=torch.uint8, device="cuda")
+    s = torch.empty((t, -(-width // 128)), device="cuda")
+    lib.mla_quantize_rows(dt(lib, act), x, width, t, width, q, width, s)
+    torch.cuda.synchronize()
+    kb = -(-width // 128)
+    padded = np.zeros((t, kb * 128), np.float32)
+    padded[:, :width] = x.float().cpu().numpy()
+    codes, scales = orc.fp8_quantize_blocks(padded)
+    assert np.array_equal(s.cpu().numpy(), scales)
+    got, want = q.cpu().numpy(), codes[:, :width]
+    assert np.array_equal(got & 0x7F, want & 0x7F)
+    assert np.array_equal(orc.e4m3_decode(got), orc.e4m3_decode(want))
+
+
+@pytest.mark.parametrize("width", [256, 250])
+def test_quantize_nan_inf_and_tiny_blocks(lib, width):
+    x = randn((5, width), 3)
+    x[0, 3] = float("nan")
+    x[1, 3] = float("inf")
+    x[2, :128] = 1e-38 * randn((128,), 4)
+    x[3, :128] = 3.3e38
+    x[4, :128] = 2.0 ** -99
+    q = torch.empty((5, width), dtype=torch.uint8, device="cuda")
+    s = torch.empty((5, 2), device="cuda")
+    lib.mla_quantize_rows(lib.MLA_F32, x, width, 5, width, q, width, s)
+    torch.cuda.synchronize()
+    v = decoded(q, s, width)
+    assert torch.isnan(v[0, :128]).all() and torch.isnan(v[1, :128]).all()
+    check_codes(q[2:], s[2:], x[2:].double(), width)
+    check_codes(q[:2, 128:].contiguous(), s[:2, 1:], x[:2, 128:].double(), width - 128)
+
+
+def test_norm_nan_row_stays_in_its_row(lib):
+    x = randn((3, 256), 3)
+    x[1, 7] = float("nan")
+    y = torch.empty_like(x)
+    lib.mla_norm_rows(lib.MLA_F32, x, 256, None, 0, None, 3, 256, 1e-6, None, 0, y, 256, None, 0, None)
+    torch.cuda.synchronize()
+    assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
+
+
+# ------------------------------------------------------------------ append of projected rows
+def rope_tables(lib, d_rope, rows):
+    c = torch.empty((rows, d_rope // 2), device="cuda")
+    s = torch.empty_like(c)
+    lib.mla_rope_table(d_rope, rows, 10000.0, c, s)
+    return c, s
+
+
+class Cache:
+    def __init__(self, lib, act, kind, d_c, d_rope, page, lengths, seed=0):
+        self.kind, self.page, self.d_c, self.d_rope = kind, page, d_c, d_rope
+        table, self.pages = wl.make_block_table(np.asarray(lengths), 0, True, np.random.default_rng(seed), page)
+        self.table = torch.as_tensor(table, device="cuda")
+        n = self.pages * page
+        code = {"f32": lib.MLA_F32, "bf16": lib.MLA_BF16, "fp8": lib.MLA_FP8_E4M3}[kind]
+        if kind == "fp8":
+            self.rows = torch.full((n, d_c), 99, dtype=torch.uint8, device="cuda")
+            self.scales = torch.full((n, d_c // 128), GUARD, device="cuda")
+            self.rope = torch.full((n, d_rope), GUARD, dtype=torch.bfloat16, device="cuda")
+        else:
+            self.rows = torch.full((n, d_c + d_rope), GUARD, dtype=act, device="cuda")
+            self.scales = self.rope = None
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.dims = lib.mla_dims(64, d_c, d_rope, 32, 32, 4, page, dt(lib, act), code, 0.1)
+        self.desc = lib.mla_cache(p(self.rows), p(self.scales), p(self.rope), self.table.data_ptr(),
+                                  table.shape[1], self.pages, table.shape[0])
+
+    def slots(self, seq, pos):
+        return self.table.long()[seq.long(), pos.long() // self.page] * self.page + pos.long() % self.page
+
+
+def run_append(lib, act, kind, d_c=512, d_rope=64, page=64, lengths=(1, 64, 130), gamma=True, pad=0, offset=0, seed=0):
+    c = Cache(lib, act, kind, d_c, d_rope, page, lengths, seed)
+    T, W = int(sum(lengths)), d_c + d_rope
+    seq = torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths)).int().cuda()
+    pos = torch.cat([torch.arange(n) for n in lengths]).int().cuda()
+    order = torch.randperm(T, generator=torch.Generator().manual_seed(seed)).cuda()
+    seq, pos = seq[order].contiguous(), pos[order].contiguous()
+    ld = W + pad
+    buf = torch.full((T * ld + offset,), GUARD, dtype=act, device="cuda")
+    kv = buf[offset:].view(T, ld)
+    kv[:, :W] = randn((T, W), seed + 1).to(act)
+    G = (1 + 0.2 * randn((d_c,), seed + 2)).to(act) if gamma else None
+    cos, sin = rope_tables(lib, d_rope, max(lengths))
+    lib.mla_append_rows(c.dims, kv, ld, T, seq, pos, G, 1e-6, cos, sin, max(lengths), c.desc)
+    torch.cuda.synchronize()
+    assert lib.mla_check_device_error()[0] == 0
+    x = kv[:, :W].double()
+    lat = x[:, :d_c]
+    if gamma:
+        lat = norm_ref(kv[:, :d_c], None, G, 1e-6)[1]
+    a, b = x[:, d_c::2], x[:, d_c + 1::2]
+    cs, sn = cos.double()[pos.long()], sin.double()[pos.long()]
+    rot = torch.stack((a * cs - b * sn, a * sn + b * cs), -1).flatten(1)
+    # two products and a sum: 3 roundings of at most U (|a| + |b|) each, then the store's
+    pair = (a.abs() + b.abs()).repeat_interleave(2, 1) * 3 * 2.0 ** -24
+    at = c.slots(seq, pos)
+    rest = torch.ones(c.pages * page, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    half = HALF[torch.bfloat16 if kind == "fp8" else act]
+    got = c.rope[at] if kind == "fp8" else c.rows[at][:, d_c:]
+    assert ((got.double() - rot).abs() <= half * rot.abs() + pair * (1 + half)).all()
+    if kind == "fp8":
+        check_codes(c.rows[at], c.scales[at], lat, d_c, REL if gamma else 2.0 ** -24)
+        assert (c.rows[rest] == 99).all() and (c.scales[rest] == GUARD).all() and (c.rope[rest] == GUARD).all()
+    else:
+        near(c.rows[at][:, :d_c], lat, REL if gamma else 0.0)
+        assert (c.rows[rest] == GUARD).all()
+
+
+KINDS = [(torch.float32, "f32"), (torch.bfloat16, "bf16"), (torch.bfloat16, "fp8")]
+
+
+@pytest.mark.parametrize("act,kind", KINDS)
+@pytest.mark.parametrize("gamma", [True, False])
+def test_append_rows(lib, act, kind, gamma):
+    run_append(lib, act, kind, gamma=gamma)
+
+
+@pytest.mark.parametrize("act,kind", KINDS)
+@pytest.mark.parametrize("lengths", [(1,), (5,), (700, 1, 3)])
+def test_append_rows_counts(lib, act, kind, lengths):
+    run_append(lib, act, kind, lengths=lengths, seed=3)
+
+
+@pytest.mark.parametrize("act,kind", KINDS)
+@pytest.mark.parametrize("d_c,d_rope,page", [(128, 16, 1), (256, 64, 16), (384, 8, 7), (1024, 256, 64), (1152, 64, 64),
+                                             (512, 2, 64), (128, 258, 3)])
+def test_append_rows_shapes(lib, act, kind, d_c, d_rope, page):
+    run_append(lib, act, kind, d_c=d_c, d_rope=d_rope, page=page, lengths=(3, 20))
+
+
+@pytest.mark.parametrize("d_c", [1, 9, 100, 520])
+def test_append_rows_odd_latent(lib, d_c):
+    run_append(lib, torch.float32, "f32", d_c=d_c, d_rope=6, lengths=(4, 9))
+    run_append(lib, torch.bfloat16, "bf16", d_c=d_c, d_rope=6, lengths=(4, 9))
+
+
+@pytest.mark.parametrize("pad,offset", [(1536, 0), (3, 0), (8, 8), (0, 1)])
+def test_append_rows_strides(lib, pad, offset):
+    for act, kind in KINDS:
+        run_append(lib, act, kind, pad=pad, offset=offset)
+
+
+def test_append_rows_bad_tokens_are_skipped(lib):
+    """A bad sequence, position or page id skips that token alone and is reported; nothing else
+    of the cache changes."""
+    for d_c, d_rope in ((512, 64), (130, 6)):
+        for what, kind in (("seq", 4), ("neg", 4), ("pos", 2), ("past", 2), ("page", 1)):
+            c = Cache(lib, torch.bfloat16, "bf16", d_c, d_rope, 64, (64, 64))
+            kv = randn((3, d_c + d_rope), 1).bfloat16()
+            seq = torch.tensor([0, 1, 1], dtype=torch.int32, device="cuda")
+            pos = torch.tensor([5, 6, 7], dtype=torch.int32, device="cuda")
+            good = c.slots(seq, pos)[[0, 2]]
+            if what == "seq":
+                seq[1] = 2
+            elif what == "neg":
+                seq[1] = -1
+            elif what == "pos":
+                pos[1] = -3
+            elif what == "past":
+                pos[1] = 64
+            else:
+                seq[1], pos[2] = 0, 7
+                good = c.slots(seq, pos)[[0, 1]]
+                c.table[1, 0] = c.pages
+            cos, sin = rope_tables(lib, d_rope, 128)
+            lib.mla_append_rows(c.dims, kv, d_c + d_rope, 3, seq, pos, None, 0.0, cos, sin, 128, c.desc)
+            status, detail = lib.mla_check_device_error()
+            assert status == 4 and detail >> 24 == kind, (what, status, detail)
+            rest = torch.ones(c.pages * 64, dtype=torch.bool, device="cuda")
+            rest[good] = False
+            assert (c.rows[rest] == GUARD).all() and not (c.rows[good] == GUARD).any()
+
+
+def test_append_rows_writes_what_append_cache_writes(lib):
+    """Same latents, same codes: the fused append's rows of an fp32 model, and append_rows on the
+    rows that its projection gives (identity weights, so the products are exact)."""
+    w = dataclasses.replace(wl.WORKLOADS["tiny_fp32"], d_model=80)
+    lengths = (5, 70)
+    T = sum(lengths)
+    h = randn((T, 80), 11)
+    eye = torch.eye(80, device="cuda")
+    seq = torch.repeat_interleave(torch.arange(2), torch.tensor(lengths)).int().cuda()
+    pos = torch.cat([torch.arange(n) for n in lengths]).int().cuda()
+    cos, sin = rope_tables(lib, 16, 128)
+    a, b = (Cache(lib, torch.float32, "f32", w.d_c, w.d_rope, 64, lengths) for _ in range(2))
+    dims = lib.mla_dims(80, 64, 16, 32, 32, 4, 64, lib.MLA_F32, lib.MLA_F32, 0.1)
+    n = lib.mla_append_workspace_size(dims, T)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    lib.mla_append_cache(dims, h, T, seq, pos, eye[:64].contiguous(), eye[64:].contiguous(), cos, sin, 128, a.desc, ws, n)
+    lib.mla_append_rows(b.dims, h, 80, T, seq, pos, None, 0.0, cos, sin, 128, b.desc)
+    torch.cuda.synchronize()
+    # the rotation may contract a product and a sum: 3 roundings
+    assert torch.equal(a.rows[:, :64], b.rows[:, :64])
+    assert ((a.rows - b.rows).abs() <= 2.0 ** -21).all()
+
+
+def test_rows_captured_and_replayed_with_new_inputs(lib):
+    t, width = 9, 1536
+    x, res = randn((t, width), 1).bfloat16(), randn((t, width), 2).bfloat16()
+    g = (1 + 0.1 * randn((width,), 3)).bfloat16()
+    q = torch.zeros((t, width), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((t, 12), device="cuda")
+    y = torch.empty_like(x)
+    st = torch.cuda.Stream()
+
+    def both():
+        lib.mla_norm_rows(lib.MLA_BF16, x, width, res, width, g, t, width, 1e-6, None, 0, y, width, None, 0, None, st)
+        lib.mla_quantize_rows(lib.MLA_BF16, y, width, t, width, q, width, s, st)
+
+    with torch.cuda.stream(st):
+        both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        both()
+    for seed in (10, 11):
+        x.copy_(randn((t, width), seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        near(y, norm_ref(x, res, g, 1e-6)[1])
+        check_codes(q, s, y.double(), width, 2.0 ** -24)
