@@ -21,5 +21,6 @@ _BINDING_NAMES = {
 def __getattr__(name):
     if name in _BINDING_NAMES:
         mod = importlib.import_module("._binding", __name__)
-        return getattr(mod, name)
+        value = globals()[name] = getattr(mod, name)  # later lookups do not come here
+        return value
     raise AttributeError(name)

@@ -5,6 +5,9 @@
 // x and w E4M3, one fp32 scale per 128 values of a row of x and per 128 x 128 block of w.  The
 // products of one block are summed without scales (exact products, fp32 sums), then the block's
 // sum is scaled and added to an fp32 accumulator.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "mla_internal.cuh"
 #include "proj_fp8.cuh"
 #include "sm100_ptx.cuh"
@@ -76,9 +79,345 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
   }
 }
 
+// ------------------------------------------------------------------ few tokens
+// Bound by reading the weights once.  They are the M = 128 operand of the MMA (TMEM lane = output),
+// the tokens its N operand (BN columns), and the S CTAs of a cluster each take a range of the
+// scale blocks, so that enough loads are in flight on every SM.  One stage is one scale block:
+// 128 weight rows and BN token rows of 128 bytes, a single row of the 128-byte swizzle.  Each
+// block's products go to a TMEM accumulator of their own (ND of them in turn); the promoting warps
+// read it, scale it by xs[t, b] ws[n / 128, b] and add it to fp32 sums in registers.  At the end
+// the S partial sums of an output meet in the shared memory of the CTA that owns its row (the
+// idle stage ring, over distributed shared memory) and are added in rank order: no workspace, no
+// atomics.
+constexpr int A_BYTES = 128 * 128;
+
+template <int BN>
+struct SkCfg {
+  static constexpr int OCC = BN <= 64 ? 2 : 1;                   // CTAs per SM
+  static constexpr int NST = BN <= 32 ? 5 : BN == 64 ? 4 : 6;
+  static constexpr int STAGE = A_BYTES + BN * 128;
+  static constexpr int ND = 4;
+  static constexpr uint32_t TCOLS = ND * BN;                     // 64 to 512 columns
+  static constexpr int PW = BN <= 64 ? 4 : 8;                    // promoting warps
+  static constexpr int CW = BN <= 64 ? BN : 64;                  // columns of one of them
+  static constexpr int XC = (PW == 4 ? 256 : 128) / CW;          // scale blocks fetched at a time
+  static constexpr int THREADS = 64 + PW * 32;
+  static constexpr int XS_OFF = NST * STAGE;                     // per warp: [2][XC][CW] fp32
+  static constexpr int BAR_OFF = XS_OFF + PW * 2 * XC * CW * 4;
+  static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  static constexpr int RLD = BN + 4;                             // receive row, floats (bank spread)
+  static_assert((128 + 8) * RLD * 4 <= NST * STAGE, "the receive buffer aliases the stage ring");
+  static_assert(OCC * (SMEM + 1024) <= 233472 && OCC * TCOLS <= 512, "CTAs per SM");
+};
+
+template <int BN>
+struct SkBars {
+  uint64_t full[SkCfg<BN>::NST], empty[SkCfg<BN>::NST], dfull[SkCfg<BN>::ND], dempty[SkCfg<BN>::ND];
+  uint32_t tmem_base;
+};
+
+struct SkParams {
+  const float* xs;
+  const float* ws;
+  int T, N, blocks, per_cta;  // blocks: scale blocks of K, per_cta of them for each CTA of a cluster
+  void* out;
+  long out_ld;
+  int out_f32;
+  int* err;
+};
+
+__device__ __forceinline__ void store_out(const SkParams& p, long t, int n, float v) {
+  if (p.out_f32)
+    static_cast<float*>(p.out)[t * p.out_ld + n] = v;
+  else
+    static_cast<__nv_bfloat16*>(p.out)[t * p.out_ld + n] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+// CN (16 or 32) consecutive fp32 columns of this thread's TMEM lane
+template <int CN>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[CN]) {
+  if constexpr (CN == 32)
+    tmem_ld32(addr, v);
+  else
+    tmem_ld16(addr, v);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
+    fp8_skinny_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                      const SkParams p) {
+  using C = SkCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  SkBars<BN>* bars = reinterpret_cast<SkBars<BN>*>(smem + C::BAR_OFF);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int S = gridDim.x, rank = blockIdx.x;
+  const int n0 = blockIdx.y * 128;
+  const int t0 = blockIdx.z * BN;
+  const int b0 = rank * p.per_cta;
+  const int nb = max(0, min(p.blocks, b0 + p.per_cta) - b0);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int d = 0; d < C::ND; ++d) {
+      mbar_init(&bars->dfull[d], 1);
+      mbar_init(&bars->dempty[d], C::PW);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, C::TCOLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // sums of this thread's lane (output n0 + 32 quarter + lane) for its CW columns, as pairs
+  uint64_t acc[C::CW / 2];
+#pragma unroll
+  for (int c = 0; c < C::CW / 2; ++c) acc[c] = 0ull;
+  const int quarter = warp & 3;
+  const int col0 = C::PW == 8 ? ((warp - 2) / 4) * C::CW : 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      // The weights' first stages come to L2 while the preceding kernel finishes (a prefetch
+      // reads nothing that could be stale); every read follows the wait.
+      for (int i = 0; i < min(nb, C::NST); ++i) tma_prefetch_l2_2d(&tm_w, (b0 + i) * 128, n0);
+      griddep_wait();
+      int issued = 0;
+      for (int i = 0; i < nb; ++i) {
+        const int s = i % C::NST;
+        if (i >= C::NST && !mbar_wait(&bars->empty[s], ((i / C::NST) - 1) & 1)) {
+          record_error(p.err, ERR_TIMEOUT, 60);
+          break;
+        }
+        uint8_t* st = smem + s * C::STAGE;
+        mbar_arrive_expect_tx(&bars->full[s], C::STAGE);
+        tma_load_2d(st, &tm_w, (b0 + i) * 128, n0, &bars->full[s]);
+        tma_load_2d(st + A_BYTES, &tm_x, (b0 + i) * 128, t0, &bars->full[s]);
+        issued = i + 1;
+      }
+      // no load of this CTA may still be in flight when the ring is reused or the CTA exits
+      for (int i = max(0, issued - C::NST); i < issued; ++i)
+        if (!mbar_wait(&bars->full[i % C::NST], (i / C::NST) & 1)) break;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc = idesc_e4m3(128, BN);
+      for (int i = 0; i < nb; ++i) {
+        const int s = i % C::NST, d = i % C::ND;
+        if ((i >= C::ND && !mbar_wait(&bars->dempty[d], ((i / C::ND) - 1) & 1)) ||
+            !mbar_wait(&bars->full[s], (i / C::NST) & 1)) {
+          record_error(p.err, ERR_TIMEOUT, 61);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = smem_addr(smem + s * C::STAGE), b = a + A_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f8(tmem + d * BN, umma_desc(a + kk * 32, 16, 1024, UMMA_SW128), umma_desc(b + kk * 32, 16, 1024, UMMA_SW128),
+                 idesc, kk > 0 ? 1u : 0u);
+        mma_commit(&bars->empty[s]);
+        mma_commit(&bars->dfull[d]);
+      }
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- promoting warps
+    griddep_wait();
+    if (threadIdx.x == 64) griddep_launch_dependents();
+    float* xw = reinterpret_cast<float*>(smem + C::XS_OFF) + (warp - 2) * 2 * C::XC * C::CW;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    // chunk ch of the tokens' scales, XC scale blocks of this warp's CW tokens, zeros past the ends
+    auto fetch = [&](int ch) {
+      for (int e = lane; e < C::XC * C::CW; e += 32) {
+        const int r = e / C::XC, kb = ch * C::XC + e % C::XC, t = t0 + col0 + r;
+        const bool in = t < p.T && kb < nb;
+        cp_async_4(smem_addr(xw + ((ch & 1) * C::XC + e % C::XC) * C::CW + r),
+                   p.xs + (in ? (long)t * p.blocks + b0 + kb : 0), in);
+      }
+      cp_async_commit();
+    };
+    const float* wsp = p.ws + (long)blockIdx.y * p.blocks + b0;
+    if (nb > 0) fetch(0);
+    float wnext = nb > 0 ? wsp[0] : 0.f;
+    for (int i = 0; i < nb; ++i) {
+      if (i % C::XC == 0) {
+        __syncwarp();  // every lane has read the chunk before the last
+        fetch(i / C::XC + 1);
+        cp_async_wait<1>();
+        __syncwarp();
+      }
+      const float w = wnext;
+      if (i + 1 < nb) wnext = wsp[i + 1];
+      const uint64_t w2 = pack2(w, w);
+      const int d = i % C::ND;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->dfull[d], (i / C::ND) & 1))) {
+        if (lane == 0) record_error(p.err, ERR_TIMEOUT, 62);
+        break;
+      }
+      tc_fence_after();
+      const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(xw + (((i / C::XC) & 1) * C::XC + i % C::XC) * C::CW);
+      constexpr int CN = BN == 16 ? 16 : 32;
+#pragma unroll
+      for (int c0 = 0; c0 < C::CW; c0 += CN) {
+        uint32_t v[CN];
+        tmem_ld<CN>(tmem + lane_off + d * BN + col0 + c0, v);
+        tmem_wait_ld();
+        if (c0 + CN == C::CW) {  // all of it read: the accumulator may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->dempty[d]);
+        }
+#pragma unroll
+        for (int c = 0; c < CN; c += 4) {
+          const ulonglong2 x = xr[(c0 + c) / 4];
+          uint64_t& a0 = acc[(c0 + c) / 2];
+          uint64_t& a1 = acc[(c0 + c) / 2 + 1];
+          a0 = fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), mul2(x.x, w2), a0);
+          a1 = fma2(pack2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), mul2(x.y, w2), a1);
+        }
+      }
+    }
+    cp_async_wait<0>();
+  }
+
+  const int m = quarter * 32 + lane;
+  if (S == 1) {
+    if (warp >= 2 && n0 + m < p.N) {
+#pragma unroll
+      for (int c = 0; c < C::CW; c += 2) {
+        float v0, v1;
+        unpack2(acc[c / 2], v0, v1);
+        const long t = t0 + col0 + c;
+        if (t < p.T) store_out(p, t, n0 + m, v0);
+        if (t + 1 < p.T) store_out(p, t + 1, n0 + m, v1);
+      }
+    }
+  } else {
+    // Row m of the tile belongs to CTA r = ((m + 1) S - 1) / 128, which owns rows
+    // [128 r / S, 128 (r + 1) / S).  Receive buffer: [S][rows of the largest share][RLD].
+    float* recv = reinterpret_cast<float*>(smem);
+    const int share = (128 + S - 1) / S;
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();  // every CTA of the cluster has finished with its ring
+    if (warp >= 2) {
+      const int r = ((m + 1) * S - 1) / 128;
+      const uint32_t dst = map_to_rank(recv, r) + (uint32_t)(((rank * share + m - r * 128 / S) * C::RLD + col0) * 4);
+#pragma unroll
+      for (int c = 0; c < C::CW; c += 4) {
+        float v0, v1, v2, v3;
+        unpack2(acc[c / 2], v0, v1);
+        unpack2(acc[c / 2 + 1], v2, v3);
+        st_cluster_v4(dst + c * 4, v0, v1, v2, v3);
+      }
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    const int lo = rank * 128 / S, rows = (rank + 1) * 128 / S - lo;
+    for (int e = threadIdx.x; e < rows * BN; e += C::THREADS) {
+      const int mr = e % rows, c = e / rows;
+      float v = 0.f;
+      for (int s = 0; s < S; ++s) v += recv[(s * share + mr) * C::RLD + c];
+      const int n = n0 + lo + mr;
+      const long t = t0 + c;
+      if (n < p.N && t < p.T) store_out(p, t, n, v);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TCOLS);
+  }
+}
+
 }  // namespace p8
 
 // ------------------------------------------------------------------ host side
+static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// 2-D map over bytes: boxes of 128 bytes x box_rows rows, 128-byte swizzle, zeros outside.
+static bool map_bytes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_rows) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
+  using C = p8::SkCfg<BN>;
+  CUtensorMap mw, mx;
+  if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN)) return kUnsupported;
+  const int blocks = (a.K + 127) / 128, tiles_n = (a.N + 127) / 128;
+  const long tiles_t = (a.T + BN - 1) / BN;
+  if (tiles_t > 65535 || tiles_n > 65535) return kUnsupported;
+  int S = 1;
+  while (S < 8 && tiles_n * tiles_t * (S + 1) <= 148 * C::OCC && (S + 1) * 2 <= blocks) ++S;
+  p8::SkParams p;
+  p.xs = a.xs;
+  p.ws = a.ws;
+  p.T = a.T;
+  p.N = a.N;
+  p.blocks = blocks;
+  p.per_cta = (blocks + S - 1) / S;
+  p.out = a.out;
+  p.out_ld = a.out_ld;
+  p.out_f32 = a.act == MLA_F32;
+  p.err = a.err;
+  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, (unsigned)tiles_t);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, p8::fp8_skinny_kernel<BN>, mw, mx, p);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 static cudaError_t launch_fp8_any(const Fp8Args& a, cudaStream_t st) {
   if ((a.T + 63) / 64 > 65535) return kUnsupported;
   cudaLaunchConfig_t cfg = {};
@@ -96,6 +435,18 @@ static cudaError_t launch_fp8_any(const Fp8Args& a, cudaStream_t st) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) { return launch_fp8_any(a, st); }
+// TMA's rules: rows of x and w start on 16-byte boundaries.
+static bool tma_layout(const Fp8Args& a) {
+  return ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15) == 0 && a.K % 16 == 0 &&
+         a.x_ld % 16 == 0;
+}
+
+cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
+  if (!tma_layout(a)) return launch_fp8_any(a, st);
+  if (a.T <= 16) return launch_skinny<16>(a, st);
+  if (a.T <= 32) return launch_skinny<32>(a, st);
+  if (a.T <= 64) return launch_skinny<64>(a, st);
+  return launch_skinny<128>(a, st);
+}
 
 }  // namespace mla
