@@ -356,34 +356,37 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
 }
 
 // ------------------------------------------------------------------ many tokens
-// Bound by the tensor pipe.  A pair of CTAs (cta_group::2) computes 256 tokens x 256 outputs: each CTA
-// loads 128 token rows and 128 weight rows of a scale block (32 KB a stage, half of what a
-// 128 x 256 tile of its own would load), the pair's MMA (M = 256, N = 256, K = 32, four per block)
-// leaves 128 tokens x 256 outputs in each CTA's TMEM.  Here the tokens are the lanes, so a thread
-// scales its columns by one number per block, xs[t, b] ws[n / 128, b]; eight promoting warps (four
-// lane quarters x two column halves, each half one block row of ws) keep 128 fp32 sums a thread,
-// while the next block's MMA fills the other half of TMEM.  Persistent over tiles; a finished tile
-// goes out through 4 KB of shared memory a warp and TMA stores.
+// Bound by the tensor pipe.  A pair of CTAs (cta_group::2) computes 256 tokens x WN outputs: each CTA
+// loads 128 token rows and WN / 2 weight rows of a scale block, and the pair's MMA (M = 256, N = WN,
+// K = 32, four per block) leaves 128 tokens x WN outputs in each CTA's TMEM.  Here the tokens are the
+// lanes, so a thread scales its columns by one or two numbers per block, xs[t, b] ws[n / 128, b].  Eight
+// promoting warps (four lane quarters x two column halves) keep WN / 2 fp32 sums a thread while
+// the next block's MMA fills the other accumulator.  Two more warps compute the scales some blocks
+// ahead.  Persistent over tiles; a finished tile goes out through 4 KB of shared memory a warp and
+// TMA stores.
+template <int WN>
 struct WdCfg {
-  static constexpr int NST = 5;
-  static constexpr int STAGE = 2 * 128 * 128;
+  static constexpr int CH = WN / 64;                   // 32-column chunks of a promoting warp
+  static constexpr int NST = 6;
+  static constexpr int STAGE = (128 + WN / 2) * 128;
   static constexpr int STG_OFF = NST * STAGE;          // 8 warps x 32 rows x 128 bytes
-  static constexpr int XS_OFF = STG_OFF + 8 * 4096;    // 8 warps x [2][XC blocks][32 tokens] fp32
-  static constexpr int XC = 8;                         // scale blocks fetched at a time
-  static constexpr int BAR_OFF = XS_OFF + 8 * 2 * XC * 128;
+  static constexpr int SC_OFF = STG_OFF + 8 * 4096;    // scales: [2][XC blocks][2 rows of ws][SLD], 128 tokens
+  static constexpr int XC = 8;                         // scale blocks made at a time
+  static constexpr int SLD = 130;                      // (bank spread of the writes)
+  static constexpr int BAR_OFF = SC_OFF + 2 * XC * 2 * SLD * 4;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
-  // warpgroup 0: TMA, MMA and two idle warps; warpgroups 1 and 2: the promoting warps, which hold 128
-  // sums and two 32-column loads a thread.  Registers at launch 384 x 168 = 64512, after the split
-  // 128 x 56 + 256 x 224 as many.
+  // warpgroup 0: TMA, MMA and two scale warps; warpgroups 1 and 2: the promoting warps, which hold WN / 2
+  // sums and as many loaded values a thread.  Registers at launch 384 x 168 = 64512, after the split
+  // 128 x 80 + 256 x 208 = 63488.
   static constexpr int THREADS = 384;
-  static constexpr int REGS_FEW = 56, REGS_MANY = 224;
+  static constexpr int REGS_FEW = 72, REGS_MANY = 216;
+  static_assert(STAGE % 1024 == 0 && SMEM <= 232448, "shared memory of one CTA per SM");
   static_assert(128 * REGS_FEW + 256 * REGS_MANY <= THREADS * 168, "register split");
-  static constexpr int GROUP = 8;                      // token tiles walked together (x stays in L2)
-  static_assert(SMEM <= 232448, "shared memory of one CTA per SM");
 };
 
+template <int WN>
 struct WdBars {
-  uint64_t full[WdCfg::NST], empty[WdCfg::NST], dfull[2], dempty[2];
+  uint64_t full[WdCfg<WN>::NST], empty[WdCfg<WN>::NST], dfull[2], dempty[2], sfull[2], sempty[2];
   uint32_t tmem_base;
 };
 
@@ -393,27 +396,30 @@ struct WdParams {
   int T, N, blocks, tiles_t, tiles_n;
   void* out;
   long out_ld;
-  int out_f32, tma_out;
   int* err;
 };
 
-// Tile `i` in walking order: groups of GROUP token tiles, within a group the outputs outside and the
+// Tile `i` in walking order: groups of WD_GROUP token tiles, within a group the outputs outside and the
 // tokens inside, so the tiles under way at one time share both operands in L2.
+constexpr int WD_GROUP = 8;  // token tiles walked together
+template <int WN>
 __device__ __forceinline__ void wd_tile(const WdParams& p, int i, int& t0, int& n0) {
-  const int per_group = WdCfg::GROUP * p.tiles_n;
+  const int per_group = WD_GROUP * p.tiles_n;
   const int g = i / per_group, r = i % per_group;
-  const int in_group = min(WdCfg::GROUP, p.tiles_t - g * WdCfg::GROUP);
-  t0 = (g * WdCfg::GROUP + r % in_group) * 256;
-  n0 = (r / in_group) * 256;
+  const int in_group = min(WD_GROUP, p.tiles_t - g * WD_GROUP);
+  t0 = (g * WD_GROUP + r % in_group) * 256;
+  n0 = (r / in_group) * WN;
 }
 
-__global__ void __launch_bounds__(WdCfg::THREADS, 1)
+template <typename T, bool TMA_OUT, int WN>
+__global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ CUtensorMap tm_out, const WdParams p) {
-  using C = WdCfg;
+  using C = WdCfg<WN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  WdBars* bars = reinterpret_cast<WdBars*>(smem + C::BAR_OFF);
+  WdBars<WN>* bars = reinterpret_cast<WdBars<WN>*>(smem + C::BAR_OFF);
+  float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)cluster_ctarank();
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -427,6 +433,8 @@ __global__ void __launch_bounds__(WdCfg::THREADS, 1)
     for (int d = 0; d < 2; ++d) {
       mbar_init(&bars->dfull[d], 1);
       mbar_init(&bars->dempty[d], 16);  // the promoting warps of both CTAs
+      mbar_init(&bars->sfull[d], 2);
+      mbar_init(&bars->sempty[d], 8);
     }
     fence_mbar_init();
   }
@@ -440,28 +448,35 @@ __global__ void __launch_bounds__(WdCfg::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
+  // (a wait for the phase before a barrier's first one returns at once)
   if (warp < 4) {
     setmaxnreg_dec<C::REGS_FEW>();
-    if (warp == 0 && lane == 0) {
+    // The TMA and the MMA warp run their loops with all lanes and issue from an elected one: issued from
+    // a one-lane branch, the four MMAs of a block and their waits took 1000 clocks of the thread's
+    // time, twice what the tensor pipe needs for them.
+    if (warp == 0) {
       // ------------------------------------------------------------ TMA producer (both CTAs)
       griddep_wait();
-      int s = 0;             // stage, and the parity of its use
+      int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
         int t0, n0;
-        wd_tile(p, tile, t0, n0);
+        wd_tile<WN>(p, tile, t0, n0);
         for (int b = 0; b < p.blocks; ++b) {
-          if (!mbar_wait(&bars->empty[s], ph ^ 1)) {  // (true at once on a barrier's first use)
-            record_error(p.err, ERR_TIMEOUT, 64);
-            ok = false;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], ph ^ 1));
+          if (!ok) {
+            if (lane == 0) record_error(p.err, ERR_TIMEOUT, 64);
             break;
           }
           uint8_t* st = smem + s * C::STAGE;
-          if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * C::STAGE);  // both CTAs' halves
           const uint32_t bar = map_to_rank(&bars->full[s], 0);
-          tma_load_2d_pair(st, &tm_x, b * 128, t0 + rank * 128, bar);
-          tma_load_2d_pair(st + A_BYTES, &tm_w, b * 128, n0 + rank * 128, bar);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * C::STAGE);  // both CTAs' halves
+            tma_load_2d_pair(st, &tm_x, b * 128, t0 + rank * 128, bar);
+            tma_load_2d_pair(st + A_BYTES, &tm_w, b * 128, n0 + rank * (WN / 2), bar);
+          }
+          __syncwarp();
           if (++s == C::NST) {
             s = 0;
             ph ^= 1;
@@ -472,39 +487,86 @@ __global__ void __launch_bounds__(WdCfg::THREADS, 1)
       // the stages' last uses, oldest first (true at once for a stage never used).
       if (rank == 0)
         for (int k = 0; k < C::NST; ++k) {
-          if (!mbar_wait(&bars->full[s], ph ^ 1)) break;
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[s], ph ^ 1))) break;
           if (++s == C::NST) {
             s = 0;
             ph ^= 1;
           }
         }
     }
-    if (warp == 1 && lane == 0 && rank == 0) {
+    if (warp == 1 && rank == 0) {
       // ------------------------------------------------------------ MMA issuer (even CTA)
-      constexpr uint32_t idesc = idesc_e4m3(256, 256);
+      constexpr uint32_t idesc = idesc_e4m3(256, WN);
+      const uint64_t a0 = umma_desc(smem_addr(smem), 16, 1024, UMMA_SW128);
+      const uint64_t w0 = umma_desc(smem_addr(smem) + A_BYTES, 16, 1024, UMMA_SW128);
       uint32_t it = 0, ph = 0;
       int s = 0;
       bool ok = true;
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
         for (int b = 0; b < p.blocks; ++b, ++it) {
           const uint32_t d = it & 1;
-          if (!mbar_wait(&bars->dempty[d], ((it >> 1) & 1) ^ 1) || !mbar_wait(&bars->full[s], ph)) {
-            record_error(p.err, ERR_TIMEOUT, 65);
-            ok = false;
+          ok = mbar_wait(&bars->full[s], ph) && mbar_wait(&bars->dempty[d], ((it >> 1) & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (lane == 0) record_error(p.err, ERR_TIMEOUT, 65);
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_addr(smem + s * C::STAGE), w = a + A_BYTES;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8_pair(tmem + d * 256, umma_desc(a + kk * 32, 16, 1024, UMMA_SW128),
-                        umma_desc(w + kk * 32, 16, 1024, UMMA_SW128), idesc, kk > 0 ? 1u : 0u);
-          mma_commit_pair(&bars->empty[s]);
-          mma_commit_pair(&bars->dfull[d]);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t step = (uint64_t)((s * C::STAGE + kk * 32) >> 4);  // (address fields are in 16 bytes)
+              mma_f8_pair(tmem + d * 256, a0 + step, w0 + step, idesc, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_pair(&bars->dfull[d]);
+            mma_commit_pair(&bars->empty[s]);
+          }
+          __syncwarp();
           if (++s == C::NST) {
             s = 0;
             ph ^= 1;
           }
+        }
+      }
+    }
+    if (warp >= 2) {
+      // ------------------------------------------------------------ scales, XC blocks at a time
+      // xs[t, b] ws[r, b] for the two block rows r that a tile's outputs can meet.  Eight lanes read the 32 bytes of a
+      // token's chunk.  Tokens and outputs past the ends take the last one's: what they give is not
+      // stored.
+      griddep_wait();
+      const int k = lane % C::XC, r0 = (warp - 2) * 64 + lane / C::XC;
+      uint32_t cnt = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+        int t0, n0;
+        wd_tile<WN>(p, tile, t0, n0);
+        const float* ws0 = p.ws + (long)(n0 / 128) * p.blocks;
+        const float* ws1 = p.ws + (long)min(n0 / 128 + 1, (p.N - 1) / 128) * p.blocks;
+        for (int b0 = 0; b0 < p.blocks; b0 += C::XC, ++cnt) {
+          const uint32_t slot = cnt & 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->sempty[slot], ((cnt >> 1) & 1) ^ 1))) {
+            if (lane == 0) record_error(p.err, ERR_TIMEOUT, 67);
+            ok = false;
+            break;
+          }
+          const int b = min(b0 + k, p.blocks - 1);
+          const float w0 = ws0[b], w1 = ws1[b];
+          float* dst = scales + (slot * C::XC + k) * 2 * C::SLD;
+#pragma unroll
+          for (int j = 0; j < 64; j += 32) {
+            float x[C::XC];
+#pragma unroll
+            for (int i = 0; i < C::XC; ++i)
+              x[i] = p.xs[(long)min(t0 + rank * 128 + r0 + j + i * (32 / C::XC), p.T - 1) * p.blocks + b];
+#pragma unroll
+            for (int i = 0; i < C::XC; ++i) {
+              dst[r0 + j + i * (32 / C::XC)] = x[i] * w0;
+              dst[C::SLD + r0 + j + i * (32 / C::XC)] = x[i] * w1;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->sfull[slot]);
         }
       }
     }
@@ -515,141 +577,107 @@ __global__ void __launch_bounds__(WdCfg::THREADS, 1)
     griddep_wait();
     if (threadIdx.x == 128) griddep_launch_dependents();
     const int quarter = warp & 3, half = (warp - 4) / 4;
-    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * (WN / 2);
     uint8_t* stg = smem + C::STG_OFF + (warp - 4) * 4096;
-    float* xw = reinterpret_cast<float*>(smem + C::XS_OFF) + (warp - 4) * 2 * C::XC * 32;
-    const int chunks = (p.blocks + C::XC - 1) / C::XC;
-    // The scales of chunk `ch` (XC blocks) of tile `tile`: this lane's token's to shared memory, buffer
-    // `buf`, and block ch XC + lane % XC of the outputs' block row in the return value.  Tokens and
-    // outputs past the ends take the last one's: what they give is not stored.
-    auto fetch = [&](int tile, int ch, int buf) -> float {
-      float w = 0.f;
-      if (tile < tiles) {
-        int t0, n0;
-        wd_tile(p, tile, t0, n0);
-        const long t = min(t0 + rank * 128 + quarter * 32 + lane, p.T - 1);
-        const float* xs = p.xs + t * p.blocks + ch * C::XC;
-#pragma unroll
-        for (int k = 0; k < C::XC; ++k)
-          if (ch * C::XC + k < p.blocks) cp_async_4(smem_addr(xw + (buf * C::XC + k) * 32 + lane), xs + k, true);
-        const int wb = min(ch * C::XC + lane % C::XC, p.blocks - 1);
-        w = p.ws[(long)(min(n0 + half * 128, p.N - 1) / 128) * p.blocks + wb];
-      }
-      cp_async_commit();
-      return w;
-    };
-    uint32_t it = 0;
+    const float* my_scales = scales + quarter * 32 + lane;
+    // all lanes' waits for a barrier
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_count(bar, parity)); };
+    uint32_t it = 0, cnt = 0;
     bool ok = true;
-    int buf = 0;
-    float wnext = fetch(pair, 0, 0), wcur = 0.f;
     for (int tile = pair; ok && tile < tiles; tile += pairs) {
       int t0, n0;
-      wd_tile(p, tile, t0, n0);
+      wd_tile<WN>(p, tile, t0, n0);
       const int row0 = t0 + rank * 128 + quarter * 32;  // this warp's first token
-      const int col0 = n0 + half * 128;
-      uint64_t acc[64];
+      const int blk0 = n0 % 128 + half * (WN / 2);  // chunk j's row of ws is (blk0 + 32 j) / 128 past n0 / 128
+      float acc[C::CH * 32];
 #pragma unroll
-      for (int c = 0; c < 64; ++c) acc[c] = 0ull;
-      for (int b = 0; b < p.blocks; ++b, ++it) {
-        if (b % C::XC == 0) {
-          // the next chunk (of this tile or the next) is on its way while this one is used
-          const int ch = b / C::XC + 1;
-          wcur = wnext;
-          __syncwarp();
-          wnext = ch < chunks ? fetch(tile, ch, buf ^ 1) : fetch(tile + pairs, 0, buf ^ 1);
-          cp_async_wait<1>();
-          buf ^= 1;  // (a lane reads only what it fetched itself)
-        }
-        const float sc = xw[((buf ^ 1) * C::XC + b % C::XC) * 32 + lane] * __shfl_sync(0xffffffffu, wcur, b % C::XC);
-        const uint64_t s2 = pack2(sc, sc);
-        const uint32_t d = it & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->dfull[d], (it >> 1) & 1))) {
-          if (lane == 0) record_error(p.err, ERR_TIMEOUT, 66);
-          ok = false;
-          break;
-        }
+      for (int c = 0; c < C::CH * 32; ++c) acc[c] = 0.f;
+      uint32_t v[C::CH][32];
+      auto ready = [&]() -> bool {  // the accumulator of block `it` is there
+        const bool r = wait(&bars->dfull[it & 1], (it >> 1) & 1);
         tc_fence_after();
-        uint32_t v[2][32];
-        tmem_ld32(taddr + d * 256, v[0]);
+        return r;
+      };
+      ok = ready();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_wait_ld32(v[q & 1]);
-          if (q < 3) {
-            tmem_ld32(taddr + d * 256 + (q + 1) * 32, v[(q + 1) & 1]);
-          } else {
-            // all of it is in registers: the accumulator may be overwritten
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(&bars->dempty[d], 0);
-          }
+      for (int j = 0; j < C::CH; ++j) tmem_ld32(taddr + (it & 1) * 256 + j * 32, v[j]);
+      for (int b0 = 0; ok && b0 < p.blocks; b0 += C::XC, ++cnt) {
+        const uint32_t slot = cnt & 1;
+        ok = wait(&bars->sfull[slot], (cnt >> 1) & 1);
+        const float* sp = my_scales + slot * (C::XC * 2 * C::SLD);
+        const int n = min(C::XC, p.blocks - b0);
+#pragma unroll 1
+        for (int k = 0; ok && k < n; ++k, sp += 2 * C::SLD) {
+          const float s0 = sp[0], s1 = sp[C::SLD];
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            uint64_t& a = acc[q * 16 + c / 2];
-            a = fma2(pack2(__uint_as_float(v[q & 1][c]), __uint_as_float(v[q & 1][c + 1])), s2, a);
-          }
-        }
-      }
-      if (!ok) break;
-      // ---- the tile: 32 tokens x 128 outputs of this warp, 128 bytes of each row at a time
-      const int per = p.out_f32 ? 32 : 64;  // outputs in 128 bytes
-#pragma unroll
-      for (int c0 = 0; c0 < 128; c0 += 32) {
-        if (p.out_f32 || c0 % 64 == 0) {  // the staging rows are free again
-          if (p.tma_out) {
-            if (lane == 0) bulk_wait_group_read<0>();
-          }
+          for (int j = 0; j < C::CH; ++j) tmem_wait_ld32(v[j]);
+          // all of it is in registers: the accumulator may be overwritten
+          tc_fence_before();
           __syncwarp();
-        }
-        const int chunk0 = p.out_f32 ? 0 : (c0 % 64) / 8;
-        if (p.out_f32) {
+          if (lane == 0) mbar_arrive_cluster_relaxed(&bars->dempty[it & 1], 0);
+          ++it;
+          const bool more = b0 + k + 1 < p.blocks;
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            ulonglong2 v = make_ulonglong2(acc[(c0 + c) / 2], acc[(c0 + c) / 2 + 1]);
-            *reinterpret_cast<ulonglong2*>(stg + lane * 128 + (((c / 4) ^ (lane & 7)) << 4)) = v;
+          for (int j = 0; j < C::CH; ++j) {
+            const float s = blk0 + 32 * j < 128 ? s0 : s1;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) acc[j * 32 + c] = fmaf(__uint_as_float(v[j][c]), s, acc[j * 32 + c]);
+            // the next block's chunk takes the registers at once
+            if (more) {
+              if (j == 0) ok = ready();
+              tmem_ld32(taddr + (it & 1) * 256 + j * 32, v[j]);
+            }
+          }
+        }
+        if (lane == 0) mbar_arrive(&bars->sempty[slot]);
+      }
+      if (!ok && lane == 0) record_error(p.err, ERR_TIMEOUT, 66);
+      if (!ok) break;
+      // ---- the tile: 32 tokens x WN / 2 outputs of this warp, 32 outputs at a time
+      constexpr int ROW = 32 * sizeof(T), NBUF = 4096 / (32 * ROW);  // bytes of a staged row; buffers
+#pragma unroll
+      for (int j = 0; j < C::CH; ++j) {
+        uint8_t* buf = stg + (j % NBUF) * 32 * ROW;
+        if (TMA_OUT && lane == 0) bulk_wait_group_read<NBUF - 1>();  // the buffer's last store has read it
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < ROW / 16; ++q) {  // 16 bytes, at the place that the 128- or 64-byte swizzle gives them
+          uint4 w;
+          if constexpr (sizeof(T) == 4) {
+            w = make_uint4(__float_as_uint(acc[j * 32 + 4 * q]), __float_as_uint(acc[j * 32 + 4 * q + 1]),
+                           __float_as_uint(acc[j * 32 + 4 * q + 2]), __float_as_uint(acc[j * 32 + 4 * q + 3]));
+          } else {
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 x = __floats2bfloat162_rn(acc[j * 32 + 8 * q + 2 * i], acc[j * 32 + 8 * q + 2 * i + 1]);
+              h[i] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            w = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          *reinterpret_cast<uint4*>(buf + lane * ROW + ((q ^ (sizeof(T) == 4 ? lane & 7 : (lane >> 1) & 3)) << 4)) = w;
+        }
+        const int cs = n0 + half * (WN / 2) + j * 32;
+        if (TMA_OUT) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.T && cs < p.N) tma_store_2d(&tm_out, buf, cs, row0);  // clipped to T x N
+            bulk_commit_group();
           }
         } else {
-#pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float lo, hi;
-              unpack2(acc[(c0 + c) / 2 + j], lo, hi);
-              const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-              w[j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(stg + lane * 128 + (((chunk0 + c / 8) ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        if (p.out_f32 || c0 % 64 == 32) {  // 128 bytes of every row are there
-          const int cs = col0 + c0 + 32 - per;
-          if (p.tma_out) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && row0 < p.T && cs < p.N) {
-              tma_store_2d(&tm_out, stg, cs, row0);  // rows past T and columns past N are not written
-              bulk_commit_group();
-            }
-          } else {
-            __syncwarp();
-            const int elt = p.out_f32 ? 4 : 2;
-            for (int r = 0; r < 32 && row0 + r < p.T; ++r)
-              for (int c = lane; c < per; c += 32) {
-                if (cs + c >= p.N) continue;
-                const uint8_t* src = stg + r * 128 + ((((c * elt) >> 4) ^ (r & 7)) << 4) + ((c * elt) & 15);
-                const long at = (long)(row0 + r) * p.out_ld + cs + c;
-                if (p.out_f32)
-                  static_cast<float*>(p.out)[at] = *reinterpret_cast<const float*>(src);
-                else
-                  static_cast<__nv_bfloat16*>(p.out)[at] = *reinterpret_cast<const __nv_bfloat16*>(src);
-              }
+          __syncwarp();
+          for (int r = 0; r < 32; ++r) {
+            const int at = lane * (int)sizeof(T);
+            if (row0 + r < p.T && cs + lane < p.N)
+              static_cast<T*>(p.out)[(long)(row0 + r) * p.out_ld + cs + lane] = *reinterpret_cast<const T*>(
+                  buf + r * ROW + (((at >> 4) ^ (sizeof(T) == 4 ? r & 7 : (r >> 1) & 3)) << 4) + (at & 15));
           }
         }
       }
     }
-    cp_async_wait<0>();
-    if (p.tma_out && lane == 0) bulk_wait_group<0>();
+    tmem_wait_ld();
+    if (TMA_OUT && lane == 0) bulk_wait_group<0>();
     __syncwarp();
   }
   tc_fence_before();
@@ -748,41 +776,44 @@ static cudaError_t launch_fp8_any(const Fp8Args& a, cudaStream_t st) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Output tiles go out by TMA stores (boxes of 128 bytes x 32 rows) where its alignment rules allow.
+// Output tiles go out by TMA stores (boxes of 32 outputs x 32 rows) where its alignment rules allow.
 static bool map_out(CUtensorMap* m, const Fp8Args& a) {
   auto enc = tmap_encoder();
   const int elt = a.act == MLA_F32 ? 4 : 2;
   if (!enc || (reinterpret_cast<uintptr_t>(a.out) & 15) || (a.out_ld * elt) % 16) return false;
   cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.T};
   cuuint64_t strides[1] = {(cuuint64_t)(a.out_ld * elt)};
-  cuuint32_t box[2] = {(cuuint32_t)(128 / elt), 32};
+  cuuint32_t box[2] = {32, 32};
   cuuint32_t es[2] = {1, 1};
   return enc(m, a.act == MLA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, elt == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int WN>
 static cudaError_t launch_wide(const Fp8Args& a, cudaStream_t st) {
-  using C = p8::WdCfg;
+  using C = p8::WdCfg<WN>;
   CUtensorMap mw, mx, mo;
-  if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, 128)) return kUnsupported;
+  if (!map_bytes(&mw, a.w, a.K, a.N, a.K, WN / 2) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, 128)) return kUnsupported;
   p8::WdParams p;
-  p.tma_out = map_out(&mo, a);
-  if (!p.tma_out) mo = mx;
+  const bool tma_out = map_out(&mo, a);
+  if (!tma_out) mo = mx;
+  auto kernel = a.act == MLA_F32 ? (tma_out ? p8::fp8_wide_kernel<float, true, WN> : p8::fp8_wide_kernel<float, false, WN>)
+                                 : (tma_out ? p8::fp8_wide_kernel<__nv_bfloat16, true, WN>
+                                            : p8::fp8_wide_kernel<__nv_bfloat16, false, WN>);
   p.xs = a.xs;
   p.ws = a.ws;
   p.T = a.T;
   p.N = a.N;
   p.blocks = (a.K + 127) / 128;
   p.tiles_t = (a.T + 255) / 256;
-  p.tiles_n = (a.N + 255) / 256;
+  p.tiles_n = (a.N + WN - 1) / WN;
   p.out = a.out;
   p.out_ld = a.out_ld;
-  p.out_f32 = a.act == MLA_F32;
   p.err = a.err;
   const long tiles = (long)p.tiles_t * p.tiles_n;
   if (tiles > (1 << 30)) return kUnsupported;
-  cudaError_t e = cudaFuncSetAttribute(p8::fp8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (tiles < 74 ? tiles : 74)));
@@ -798,7 +829,7 @@ static cudaError_t launch_wide(const Fp8Args& a, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, p8::fp8_wide_kernel, mw, mx, mo, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, mw, mx, mo, p);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -815,7 +846,7 @@ cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
   if (a.T <= 32) return launch_skinny<32>(a, st);
   if (a.T <= 64) return launch_skinny<64>(a, st);
   if (a.T <= 128) return launch_skinny<128>(a, st);
-  return launch_wide(a, st);
+  return launch_wide<192>(a, st);
 }
 
 }  // namespace mla

@@ -101,6 +101,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// The same wait bounded by a count instead of the clock: 2^20 tries that each sleep up to about 2 us
+// (2 s in all).  It keeps one register alive instead of six, for loops that have none to spare.
+__device__ __forceinline__ bool mbar_wait_count(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i)
+    if (mbar_try_wait_sleep<false>(bar, parity, 2000u)) return true;
+  return false;
+}
+
 // Non-blocking probe of a phase (CTA scope).
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -117,6 +126,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 // ------------------------------------------------------------------ cluster
