@@ -366,7 +366,9 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
 // TMA stores.
 template <int WN>
 struct WdCfg {
-  static constexpr int CH = WN / 64;                   // 32-column chunks of a promoting warp
+  static constexpr int HC = WN / 2;                    // columns of a promoting warp
+  static constexpr int NF = HC / 32, TAIL = HC % 32;   // loaded as 32s and a 16
+  static constexpr int ND = 512 / WN;                  // accumulators
   static constexpr int NST = 6;
   static constexpr int STAGE = (128 + WN / 2) * 128;
   static constexpr int STG_OFF = NST * STAGE;          // 8 warps x 32 rows x 128 bytes
@@ -380,13 +382,14 @@ struct WdCfg {
   // 128 x 80 + 256 x 208 = 63488.
   static constexpr int THREADS = 384;
   static constexpr int REGS_FEW = 72, REGS_MANY = 216;
-  static_assert(STAGE % 1024 == 0 && SMEM <= 232448, "shared memory of one CTA per SM");
+  static_assert((TAIL == 0 || TAIL == 16) && STAGE % 1024 == 0 && SMEM <= 232448, "shared memory of one CTA per SM");
   static_assert(128 * REGS_FEW + 256 * REGS_MANY <= THREADS * 168, "register split");
 };
 
 template <int WN>
 struct WdBars {
-  uint64_t full[WdCfg<WN>::NST], empty[WdCfg<WN>::NST], dfull[2], dempty[2], sfull[2], sempty[2];
+  uint64_t full[WdCfg<WN>::NST], empty[WdCfg<WN>::NST], dfull[WdCfg<WN>::ND], dempty[WdCfg<WN>::ND];
+  uint64_t sfull[2], sempty[2];
   uint32_t tmem_base;
 };
 
@@ -430,9 +433,11 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
-    for (int d = 0; d < 2; ++d) {
+    for (int d = 0; d < C::ND; ++d) {
       mbar_init(&bars->dfull[d], 1);
       mbar_init(&bars->dempty[d], 16);  // the promoting warps of both CTAs
+    }
+    for (int d = 0; d < 2; ++d) {
       mbar_init(&bars->sfull[d], 2);
       mbar_init(&bars->sempty[d], 8);
     }
@@ -499,13 +504,12 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
       constexpr uint32_t idesc = idesc_e4m3(256, WN);
       const uint64_t a0 = umma_desc(smem_addr(smem), 16, 1024, UMMA_SW128);
       const uint64_t w0 = umma_desc(smem_addr(smem) + A_BYTES, 16, 1024, UMMA_SW128);
-      uint32_t it = 0, ph = 0;
-      int s = 0;
-      bool ok = true;
+      uint32_t ph = 0, dph = 0;  // parities of the current uses of stage s and accumulator d
+      int s = 0, d = 0;
+      bool ok = true, loaded = false, freed = false;  // asked while the block before is issued
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
-        for (int b = 0; b < p.blocks; ++b, ++it) {
-          const uint32_t d = it & 1;
-          ok = mbar_wait(&bars->full[s], ph) && mbar_wait(&bars->dempty[d], ((it >> 1) & 1) ^ 1);
+        for (int b = 0; b < p.blocks; ++b) {
+          ok = (loaded || mbar_wait(&bars->full[s], ph)) && (freed || mbar_wait(&bars->dempty[d], dph ^ 1));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
             if (lane == 0) record_error(p.err, ERR_TIMEOUT, 65);
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint64_t step = (uint64_t)((s * C::STAGE + kk * 32) >> 4);  // (address fields are in 16 bytes)
-              mma_f8_pair(tmem + d * 256, a0 + step, w0 + step, idesc, kk > 0 ? 1u : 0u);
+              mma_f8_pair(tmem + d * WN, a0 + step, w0 + step, idesc, kk > 0 ? 1u : 0u);
             }
             mma_commit_pair(&bars->dfull[d]);
             mma_commit_pair(&bars->empty[s]);
@@ -526,6 +530,12 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
             s = 0;
             ph ^= 1;
           }
+          if (++d == C::ND) {
+            d = 0;
+            dph ^= 1;
+          }
+          loaded = mbar_test(&bars->full[s], ph);
+          freed = mbar_test(&bars->dempty[d], dph ^ 1);
         }
       }
     }
@@ -577,30 +587,38 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
     griddep_wait();
     if (threadIdx.x == 128) griddep_launch_dependents();
     const int quarter = warp & 3, half = (warp - 4) / 4;
-    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * (WN / 2);
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::HC;
     uint8_t* stg = smem + C::STG_OFF + (warp - 4) * 4096;
     const float* my_scales = scales + quarter * 32 + lane;
     // all lanes' waits for a barrier
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_count(bar, parity)); };
-    uint32_t it = 0, cnt = 0;
+    uint32_t cnt = 0, dph = 0;  // chunks of scales used; parity of the current use of accumulator d
+    int d = 0;
     bool ok = true;
     for (int tile = pair; ok && tile < tiles; tile += pairs) {
       int t0, n0;
       wd_tile<WN>(p, tile, t0, n0);
       const int row0 = t0 + rank * 128 + quarter * 32;  // this warp's first token
-      const int blk0 = n0 % 128 + half * (WN / 2);  // chunk j's row of ws is (blk0 + 32 j) / 128 past n0 / 128
-      float acc[C::CH * 32];
+      const int blk0 = n0 % 128 + half * C::HC;  // column c's row of ws is (blk0 + c) / 128 past n0 / 128
+      float acc[C::HC];
 #pragma unroll
-      for (int c = 0; c < C::CH * 32; ++c) acc[c] = 0.f;
-      uint32_t v[C::CH][32];
-      auto ready = [&]() -> bool {  // the accumulator of block `it` is there
-        const bool r = wait(&bars->dfull[it & 1], (it >> 1) & 1);
+      for (int c = 0; c < C::HC; ++c) acc[c] = 0.f;
+      uint32_t v[C::NF][32], vt[16];
+      auto load = [&](int j) {  // chunk j of accumulator d
+        if (j < C::NF)
+          tmem_ld32(taddr + d * WN + j * 32, v[j]);
+        else
+          tmem_ld16(taddr + d * WN + j * 32, vt);
+      };
+      auto ready = [&]() -> bool {  // accumulator d is there
+        const bool r = wait(&bars->dfull[d], dph);
         tc_fence_after();
         return r;
       };
+      constexpr int CH = C::NF + (C::TAIL ? 1 : 0);
       ok = ready();
 #pragma unroll
-      for (int j = 0; j < C::CH; ++j) tmem_ld32(taddr + (it & 1) * 256 + j * 32, v[j]);
+      for (int j = 0; j < CH; ++j) load(j);
       for (int b0 = 0; ok && b0 < p.blocks; b0 += C::XC, ++cnt) {
         const uint32_t slot = cnt & 1;
         ok = wait(&bars->sfull[slot], (cnt >> 1) & 1);
@@ -609,23 +627,36 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
 #pragma unroll 1
         for (int k = 0; ok && k < n; ++k, sp += 2 * C::SLD) {
           const float s0 = sp[0], s1 = sp[C::SLD];
+          const int freed = d;
+          if (++d == C::ND) {
+            d = 0;
+            dph ^= 1;
+          }
+          const bool there = mbar_test(&bars->dfull[d], dph);  // (asked now, answered behind the first sums)
 #pragma unroll
-          for (int j = 0; j < C::CH; ++j) tmem_wait_ld32(v[j]);
+          for (int j = 0; j < C::NF; ++j) tmem_wait_ld32(v[j]);
+          if (C::TAIL) tmem_wait_ld16(vt);
           // all of it is in registers: the accumulator may be overwritten
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(&bars->dempty[it & 1], 0);
-          ++it;
+          if (lane == 0) mbar_arrive_cluster_relaxed(&bars->dempty[freed], 0);
           const bool more = b0 + k + 1 < p.blocks;
 #pragma unroll
-          for (int j = 0; j < C::CH; ++j) {
-            const float s = blk0 + 32 * j < 128 ? s0 : s1;
+          for (int j = 0; j < CH; ++j) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) acc[j * 32 + c] = fmaf(__uint_as_float(v[j][c]), s, acc[j * 32 + c]);
+            for (int c = 0; c < 32 && j * 32 + c < C::HC; ++c) {
+              const float s = blk0 + j * 32 + c / 16 * 16 < 128 ? s0 : s1;  // (rows of ws change at multiples of 16)
+              acc[j * 32 + c] = fmaf(__uint_as_float(j < C::NF ? v[j < C::NF ? j : 0][c] : vt[c % 16]), s, acc[j * 32 + c]);
+            }
             // the next block's chunk takes the registers at once
             if (more) {
-              if (j == 0) ok = ready();
-              tmem_ld32(taddr + (it & 1) * 256 + j * 32, v[j]);
+              if (j == 0) {
+                if (__all_sync(0xffffffffu, there))
+                  tc_fence_after();
+                else
+                  ok = ready();
+              }
+              load(j);
             }
           }
         }
@@ -633,31 +664,31 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
       }
       if (!ok && lane == 0) record_error(p.err, ERR_TIMEOUT, 66);
       if (!ok) break;
-      // ---- the tile: 32 tokens x WN / 2 outputs of this warp, 32 outputs at a time
-      constexpr int ROW = 32 * sizeof(T), NBUF = 4096 / (32 * ROW);  // bytes of a staged row; buffers
+      // ---- the tile: 32 tokens x WN / 2 outputs of this warp, 16 outputs at a time
+      constexpr int ROW = 16 * sizeof(T), NBUF = 4096 / (32 * ROW);  // bytes of a staged row; buffers
 #pragma unroll
-      for (int j = 0; j < C::CH; ++j) {
+      for (int j = 0; j < C::HC / 16; ++j) {
         uint8_t* buf = stg + (j % NBUF) * 32 * ROW;
         if (TMA_OUT && lane == 0) bulk_wait_group_read<NBUF - 1>();  // the buffer's last store has read it
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < ROW / 16; ++q) {  // 16 bytes, at the place that the 128- or 64-byte swizzle gives them
+        for (int q = 0; q < ROW / 16; ++q) {  // 16 bytes, at the place that the 64- or 32-byte swizzle gives them
           uint4 w;
           if constexpr (sizeof(T) == 4) {
-            w = make_uint4(__float_as_uint(acc[j * 32 + 4 * q]), __float_as_uint(acc[j * 32 + 4 * q + 1]),
-                           __float_as_uint(acc[j * 32 + 4 * q + 2]), __float_as_uint(acc[j * 32 + 4 * q + 3]));
+            w = make_uint4(__float_as_uint(acc[j * 16 + 4 * q]), __float_as_uint(acc[j * 16 + 4 * q + 1]),
+                           __float_as_uint(acc[j * 16 + 4 * q + 2]), __float_as_uint(acc[j * 16 + 4 * q + 3]));
           } else {
             uint32_t h[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(acc[j * 32 + 8 * q + 2 * i], acc[j * 32 + 8 * q + 2 * i + 1]);
+              const __nv_bfloat162 x = __floats2bfloat162_rn(acc[j * 16 + 8 * q + 2 * i], acc[j * 16 + 8 * q + 2 * i + 1]);
               h[i] = *reinterpret_cast<const uint32_t*>(&x);
             }
             w = make_uint4(h[0], h[1], h[2], h[3]);
           }
-          *reinterpret_cast<uint4*>(buf + lane * ROW + ((q ^ (sizeof(T) == 4 ? lane & 7 : (lane >> 1) & 3)) << 4)) = w;
+          *reinterpret_cast<uint4*>(buf + lane * ROW + ((q ^ (sizeof(T) == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1)) << 4)) = w;
         }
-        const int cs = n0 + half * (WN / 2) + j * 32;
+        const int cs = n0 + half * C::HC + j * 16;
         if (TMA_OUT) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -667,11 +698,11 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
           }
         } else {
           __syncwarp();
-          for (int r = 0; r < 32; ++r) {
-            const int at = lane * (int)sizeof(T);
-            if (row0 + r < p.T && cs + lane < p.N)
-              static_cast<T*>(p.out)[(long)(row0 + r) * p.out_ld + cs + lane] = *reinterpret_cast<const T*>(
-                  buf + r * ROW + (((at >> 4) ^ (sizeof(T) == 4 ? r & 7 : (r >> 1) & 3)) << 4) + (at & 15));
+          for (int e = lane; e < 32 * 16; e += 32) {
+            const int r = e / 16, c = e % 16, at = c * (int)sizeof(T);
+            if (row0 + r < p.T && cs + c < p.N)
+              static_cast<T*>(p.out)[(long)(row0 + r) * p.out_ld + cs + c] = *reinterpret_cast<const T*>(
+                  buf + r * ROW + (((at >> 4) ^ (sizeof(T) == 4 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4) + (at & 15));
           }
         }
       }
@@ -776,17 +807,17 @@ static cudaError_t launch_fp8_any(const Fp8Args& a, cudaStream_t st) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Output tiles go out by TMA stores (boxes of 32 outputs x 32 rows) where its alignment rules allow.
+// Output tiles go out by TMA stores (boxes of 16 outputs x 32 rows) where its alignment rules allow.
 static bool map_out(CUtensorMap* m, const Fp8Args& a) {
   auto enc = tmap_encoder();
   const int elt = a.act == MLA_F32 ? 4 : 2;
   if (!enc || (reinterpret_cast<uintptr_t>(a.out) & 15) || (a.out_ld * elt) % 16) return false;
   cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.T};
   cuuint64_t strides[1] = {(cuuint64_t)(a.out_ld * elt)};
-  cuuint32_t box[2] = {32, 32};
+  cuuint32_t box[2] = {16, 32};
   cuuint32_t es[2] = {1, 1};
   return enc(m, a.act == MLA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, elt == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, elt == 4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -846,7 +877,7 @@ cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
   if (a.T <= 32) return launch_skinny<32>(a, st);
   if (a.T <= 64) return launch_skinny<64>(a, st);
   if (a.T <= 128) return launch_skinny<128>(a, st);
-  return launch_wide<192>(a, st);
+  return launch_wide<160>(a, st);
 }
 
 }  // namespace mla
