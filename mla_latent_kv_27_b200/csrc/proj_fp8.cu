@@ -8,6 +8,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "mla_internal.cuh"
 #include "proj_fp8.cuh"
 #include "sm100_ptx.cuh"
@@ -85,34 +87,38 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
 // scale blocks, so that enough loads are in flight on every SM.  One stage is one scale block:
 // 128 weight rows and BN token rows of 128 bytes, a single row of the 128-byte swizzle.  Each
 // block's products go to a TMEM accumulator of their own (ND of them in turn); the promoting warps
-// read it, scale it by xs[t, b] ws[n / 128, b] and add it to fp32 sums in registers.  At the end
-// the S partial sums of an output meet in the shared memory of the CTA that owns its row (the
-// idle stage ring, over distributed shared memory) and are added in rank order: no workspace, no
-// atomics.
+// (four lane quarters x column groups) read it, scale its columns by xs[t, b] ws[n / 128, b] (made by
+// a warp of its own, XC blocks at a time) and add it to fp32 sums in registers.  At the end each
+// CTA lays its sums out in its idle stage ring and sends every other CTA the rows that one owns, one bulk
+// copy each into a buffer of the owner's shared memory; the owner adds the S partial sums of its rows
+// in rank order and stores them: no workspace, no atomics.
 constexpr int A_BYTES = 128 * 128;
 
 template <int BN>
 struct SkCfg {
-  static constexpr int OCC = BN <= 64 ? 2 : 1;                   // CTAs per SM
-  static constexpr int NST = BN <= 32 ? 5 : BN == 64 ? 4 : 6;
+  static constexpr int OCC = BN <= 32 ? 2 : 1;          // CTAs per SM
+  static constexpr int NST = BN == 16 ? 5 : BN == 64 ? 7 : 4;
   static constexpr int STAGE = A_BYTES + BN * 128;
   static constexpr int ND = 4;
-  static constexpr uint32_t TCOLS = ND * BN;                     // 64 to 512 columns
-  static constexpr int PW = BN <= 64 ? 4 : 8;                    // promoting warps
-  static constexpr int CW = BN <= 64 ? BN : 64;                  // columns of one of them
-  static constexpr int XC = (PW == 4 ? 256 : 128) / CW;          // scale blocks fetched at a time
-  static constexpr int THREADS = 64 + PW * 32;
-  static constexpr int XS_OFF = NST * STAGE;                     // per warp: [2][XC][CW] fp32
-  static constexpr int BAR_OFF = XS_OFF + PW * 2 * XC * CW * 4;
+  static constexpr uint32_t TCOLS = ND * BN;            // 64 to 512 columns
+  static constexpr int PW = BN <= 32 ? 8 : 16;          // promoting warps: four lane quarters x column groups
+  static constexpr int CW = BN / (PW / 4);              // columns of one of them
+  static constexpr int XC = 8;                          // scale blocks made at a time
+  static constexpr int SLD = BN + 4;
+  static constexpr int THREADS = 128 + PW * 32;         // warps 0 TMA, 1 MMA, 2 scales, 4 and up promoting
+  static constexpr int SC_OFF = NST * STAGE;            // scales: [2][XC][SLD] fp32
+  static constexpr int RLD = BN + 4;                    // floats of a row of partial sums (bank spread)
+  static constexpr int RECV_OFF = SC_OFF + 2 * XC * SLD * 4;      // [S][rows of the largest share][RLD]
+  static constexpr int BAR_OFF = RECV_OFF + (128 + 7) * RLD * 4;  // (S ceil(128 / S) is at most 135 for S <= 8)
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
-  static constexpr int RLD = BN + 4;                             // receive row, floats (bank spread)
-  static_assert((128 + 8) * RLD * 4 <= NST * STAGE, "the receive buffer aliases the stage ring");
+  static_assert(128 * RLD * 4 <= NST * STAGE && RECV_OFF % 16 == 0 && BAR_OFF % 8 == 0, "layout");
   static_assert(OCC * (SMEM + 1024) <= 233472 && OCC * TCOLS <= 512, "CTAs per SM");
 };
 
 template <int BN>
 struct SkBars {
   uint64_t full[SkCfg<BN>::NST], empty[SkCfg<BN>::NST], dfull[SkCfg<BN>::ND], dempty[SkCfg<BN>::ND];
+  uint64_t sfull[2], sempty[2], received;
   uint32_t tmem_base;
 };
 
@@ -134,24 +140,28 @@ __device__ __forceinline__ void store_out(const SkParams& p, long t, int n, floa
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
-               : "memory");
-}
-// CN (16 or 32) consecutive fp32 columns of this thread's TMEM lane, and the wait for them
+// CN (8, 16 or 32) consecutive fp32 columns of this thread's TMEM lane, and the wait for them
 template <int CN>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[CN]) {
   if constexpr (CN == 32)
     tmem_ld32(addr, v);
-  else
+  else if constexpr (CN == 16)
     tmem_ld16(addr, v);
+  else
+    tmem_ld8(addr, v);
 }
 template <int CN>
 __device__ __forceinline__ void tmem_wait(uint32_t (&v)[CN]) {
   if constexpr (CN == 32)
     tmem_wait_ld32(v);
-  else
+  else if constexpr (CN == 16)
     tmem_wait_ld16(v);
+  else
+    tmem_wait_ld8(v);
+}
+// a bounded wait of all lanes of a warp, the same answer in each
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 
 template <int BN>
@@ -162,14 +172,20 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   SkBars<BN>* bars = reinterpret_cast<SkBars<BN>*>(smem + C::BAR_OFF);
+  float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int S = gridDim.x, rank = blockIdx.x;
   const int n0 = blockIdx.y * 128;
   const int t0 = blockIdx.z * BN;
   const int b0 = rank * p.per_cta;
   const int nb = max(0, min(p.blocks, b0 + p.per_cta) - b0);
+  // CTA r of the cluster owns rows [128 r / S, 128 (r + 1) / S) of the tile
+  const int lo = rank * 128 / S, rows = (rank + 1) * 128 / S - lo, share = (128 + S - 1) / S;
 
-  if (threadIdx.x == 0) {
+  // The weights' first stages come to L2 while the preceding kernel finishes (a prefetch reads nothing
+  // that could be stale); every read follows the wait.
+  if (warp == 0 && lane < min(nb, C::NST)) tma_prefetch_l2_2d(&tm_w, (b0 + lane) * 128, n0);
+  if (warp == 2 && lane == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
@@ -178,7 +194,13 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
       mbar_init(&bars->dfull[d], 1);
       mbar_init(&bars->dempty[d], C::PW);
     }
+    for (int d = 0; d < 2; ++d) {
+      mbar_init(&bars->sfull[d], 1);
+      mbar_init(&bars->sempty[d], C::PW);
+    }
+    mbar_init(&bars->received, 1);
     fence_mbar_init();
+    if (S > 1) mbar_arrive_expect_tx(&bars->received, (uint32_t)(S * rows * C::RLD * 4));
   }
   if (warp == 1) {
     tmem_alloc(&bars->tmem_base, C::TCOLS);
@@ -187,6 +209,7 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (S > 1) cluster_arrive();  // peers may send to this CTA after this
   const uint32_t tmem = bars->tmem_base;
 
   // sums of this thread's lane (output n0 + 32 quarter + lane) for its CW columns, as pairs
@@ -194,96 +217,118 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
 #pragma unroll
   for (int c = 0; c < C::CW / 2; ++c) acc[c] = 0ull;
   const int quarter = warp & 3;
-  const int col0 = C::PW == 8 ? ((warp - 2) / 4) * C::CW : 0;
+  const int col0 = warp >= 4 ? (warp - 4) / 4 * C::CW : 0;
 
+  // (a wait for the phase before a barrier's first one returns at once)
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ TMA producer
-      // The weights' first stages come to L2 while the preceding kernel finishes (a prefetch
-      // reads nothing that could be stale); every read follows the wait.
-      for (int i = 0; i < min(nb, C::NST); ++i) tma_prefetch_l2_2d(&tm_w, (b0 + i) * 128, n0);
-      griddep_wait();
-      int issued = 0;
-      for (int i = 0; i < nb; ++i) {
-        const int s = i % C::NST;
-        if (i >= C::NST && !mbar_wait(&bars->empty[s], ((i / C::NST) - 1) & 1)) {
-          record_error(p.err, ERR_TIMEOUT, 60);
-          break;
-        }
+    // -------------------------------------------------------------- TMA producer
+    griddep_wait();
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nb; ++i) {
+      if (!warp_wait(&bars->empty[s], ph ^ 1)) {
+        if (lane == 0) record_error(p.err, ERR_TIMEOUT, 60);
+        break;
+      }
+      if (elect_one()) {
         uint8_t* st = smem + s * C::STAGE;
         mbar_arrive_expect_tx(&bars->full[s], C::STAGE);
         tma_load_2d(st, &tm_w, (b0 + i) * 128, n0, &bars->full[s]);
         tma_load_2d(st + A_BYTES, &tm_x, (b0 + i) * 128, t0, &bars->full[s]);
-        issued = i + 1;
       }
-      // no load of this CTA may still be in flight when the ring is reused or the CTA exits
-      for (int i = max(0, issued - C::NST); i < issued; ++i)
-        if (!mbar_wait(&bars->full[i % C::NST], (i / C::NST) & 1)) break;
+      __syncwarp();
+      if (++s == C::NST) {
+        s = 0;
+        ph ^= 1;
+      }
     }
-    __syncwarp();
+    // no load of this CTA may still be in flight when the ring is reused or the CTA exits: the stages'
+    // last uses, oldest first (true at once for a stage never used)
+    for (int k = 0; k < C::NST; ++k) {
+      if (!warp_wait(&bars->full[s], ph ^ 1)) break;
+      if (++s == C::NST) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = idesc_e4m3(128, BN);
-      for (int i = 0; i < nb; ++i) {
-        const int s = i % C::NST, d = i % C::ND;
-        if ((i >= C::ND && !mbar_wait(&bars->dempty[d], ((i / C::ND) - 1) & 1)) ||
-            !mbar_wait(&bars->full[s], (i / C::NST) & 1)) {
-          record_error(p.err, ERR_TIMEOUT, 61);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a = smem_addr(smem + s * C::STAGE), b = a + A_BYTES;
+    // -------------------------------------------------------------- MMA issuer (all lanes, an elected one issues)
+    constexpr uint32_t idesc = idesc_e4m3(128, BN);
+    const uint64_t a0 = umma_desc(smem_addr(smem), 16, 1024, UMMA_SW128);
+    const uint64_t x0 = umma_desc(smem_addr(smem) + A_BYTES, 16, 1024, UMMA_SW128);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nb; ++i) {
+      const int d = i % C::ND;
+      if (!warp_wait(&bars->dempty[d], ((i / C::ND) & 1) ^ 1) || !warp_wait(&bars->full[s], ph)) {
+        if (lane == 0) record_error(p.err, ERR_TIMEOUT, 61);
+        break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t at = (uint64_t)((s * C::STAGE) >> 4);  // (address fields are in 16 bytes)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_f8(tmem + d * BN, umma_desc(a + kk * 32, 16, 1024, UMMA_SW128), umma_desc(b + kk * 32, 16, 1024, UMMA_SW128),
-                 idesc, kk > 0 ? 1u : 0u);
+          mma_f8(tmem + d * BN, a0 + at + 2 * kk, x0 + at + 2 * kk, idesc, kk > 0 ? 1u : 0u);
         mma_commit(&bars->empty[s]);
         mma_commit(&bars->dfull[d]);
       }
+      __syncwarp();
+      if (++s == C::NST) {
+        s = 0;
+        ph ^= 1;
+      }
     }
-    __syncwarp();
-  } else {
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- scales of the CTA's tokens
+    // Eight lanes read the 32 bytes of a token's chunk.  Past the last token: zero.
+    griddep_wait();
+    const float* ws = p.ws + (long)blockIdx.y * p.blocks;
+    for (int c = 0; c * C::XC < nb; ++c) {
+      if (!warp_wait(&bars->sempty[c & 1], ((c >> 1) & 1) ^ 1)) {
+        if (lane == 0) record_error(p.err, ERR_TIMEOUT, 63);
+        break;
+      }
+      const int k = lane % C::XC, b = min(b0 + c * C::XC + k, p.blocks - 1);
+      const float w = ws[b];
+      float* dst = scales + ((c & 1) * C::XC + k) * C::SLD;
+#pragma unroll
+      for (int r0 = 0; r0 < BN; r0 += 32) {
+        float x[C::XC];
+#pragma unroll
+        for (int j = 0; j < C::XC; ++j) {
+          const int r = r0 + lane / C::XC + j * (32 / C::XC);
+          x[j] = r < BN && t0 + r < p.T ? p.xs[(long)(t0 + r) * p.blocks + b] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < C::XC; ++j) {
+          const int r = r0 + lane / C::XC + j * (32 / C::XC);
+          if (r < BN) dst[r] = x[j] * w;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->sfull[c & 1]);
+    }
+  } else if (warp >= 4) {
     // -------------------------------------------------------------- promoting warps
     griddep_wait();
-    if (threadIdx.x == 64) griddep_launch_dependents();
-    float* xw = reinterpret_cast<float*>(smem + C::XS_OFF) + (warp - 2) * 2 * C::XC * C::CW;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    // chunk ch of the tokens' scales, XC scale blocks of this warp's CW tokens, zeros past the ends
-    auto fetch = [&](int ch) {
-      for (int e = lane; e < C::XC * C::CW; e += 32) {
-        const int r = e / C::XC, kb = ch * C::XC + e % C::XC, t = t0 + col0 + r;
-        const bool in = t < p.T && kb < nb;
-        cp_async_4(smem_addr(xw + ((ch & 1) * C::XC + e % C::XC) * C::CW + r),
-                   p.xs + (in ? (long)t * p.blocks + b0 + kb : 0), in);
-      }
-      cp_async_commit();
-    };
-    const float* wsp = p.ws + (long)blockIdx.y * p.blocks + b0;
-    if (nb > 0) fetch(0);
-    float wnext = nb > 0 ? wsp[0] : 0.f;
+    if (threadIdx.x == 128) griddep_launch_dependents();
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + col0;
     for (int i = 0; i < nb; ++i) {
-      if (i % C::XC == 0) {
-        __syncwarp();  // every lane has read the chunk before the last
-        fetch(i / C::XC + 1);
-        cp_async_wait<1>();
-        __syncwarp();
-      }
-      const float w = wnext;
-      if (i + 1 < nb) wnext = wsp[i + 1];
-      const uint64_t w2 = pack2(w, w);
-      const int d = i % C::ND;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->dfull[d], (i / C::ND) & 1))) {
+      const int c = i / C::XC, d = i % C::ND;
+      if ((i % C::XC == 0 && !warp_wait(&bars->sfull[c & 1], (c >> 1) & 1)) ||
+          !warp_wait(&bars->dfull[d], (i / C::ND) & 1)) {
         if (lane == 0) record_error(p.err, ERR_TIMEOUT, 62);
         break;
       }
       tc_fence_after();
-      const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(xw + (((i / C::XC) & 1) * C::XC + i % C::XC) * C::CW);
-      constexpr int CN = BN == 16 ? 16 : 32;
+      const ulonglong2* xr =
+          reinterpret_cast<const ulonglong2*>(scales + ((c & 1) * C::XC + i % C::XC) * C::SLD + col0);
+      constexpr int CN = C::CW < 16 ? C::CW : 16;
 #pragma unroll
       for (int c0 = 0; c0 < C::CW; c0 += CN) {
         uint32_t v[CN];
-        tmem_ld<CN>(tmem + lane_off + d * BN + col0 + c0, v);
+        tmem_ld<CN>(taddr + d * BN + c0, v);
         tmem_wait<CN>(v);
         if (c0 + CN == C::CW) {  // all of it read: the accumulator may be overwritten
           tc_fence_before();
@@ -291,60 +336,67 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
           if (lane == 0) mbar_arrive(&bars->dempty[d]);
         }
 #pragma unroll
-        for (int c = 0; c < CN; c += 4) {
-          const ulonglong2 x = xr[(c0 + c) / 4];
-          uint64_t& a0 = acc[(c0 + c) / 2];
-          uint64_t& a1 = acc[(c0 + c) / 2 + 1];
-          a0 = fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), mul2(x.x, w2), a0);
-          a1 = fma2(pack2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), mul2(x.y, w2), a1);
+        for (int q = 0; q < CN; q += 4) {
+          const ulonglong2 x = xr[(c0 + q) / 4];
+          uint64_t& s0 = acc[(c0 + q) / 2];
+          uint64_t& s1 = acc[(c0 + q) / 2 + 1];
+          s0 = fma2(pack2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])), x.x, s0);
+          s1 = fma2(pack2(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3])), x.y, s1);
         }
       }
+      if (i % C::XC == C::XC - 1) {  // (the CTA's last chunk is not written again)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->sempty[c & 1]);
+      }
     }
-    cp_async_wait<0>();
   }
 
-  const int m = quarter * 32 + lane;
-  if (S == 1) {
-    if (warp >= 2 && n0 + m < p.N) {
+  // ---- partial sums [128 rows][RLD] over this CTA's own ring, idle since its last MMA completed
+  float* part = reinterpret_cast<float*>(smem);
+  float* recv = reinterpret_cast<float*>(smem + C::RECV_OFF);
+  __syncwarp();
+  if (S > 1) cluster_wait();  // (every CTA of the cluster has begun)
+  if (warp >= 4) {
+    float* dst = part + (quarter * 32 + lane) * C::RLD + col0;
 #pragma unroll
-      for (int c = 0; c < C::CW; c += 2) {
-        float v0, v1;
-        unpack2(acc[c / 2], v0, v1);
-        const long t = t0 + col0 + c;
-        if (t < p.T) store_out(p, t, n0 + m, v0);
-        if (t + 1 < p.T) store_out(p, t + 1, n0 + m, v1);
-      }
+    for (int c = 0; c < C::CW; c += 4)
+      *reinterpret_cast<ulonglong2*>(dst + c) = make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
+    fence_proxy_async_smem();
+    named_bar_sync(1, C::PW * 32);
+    if (S > 1 && warp == 4 && lane < S) {
+      const int first = lane * 128 / S, n = (lane + 1) * 128 / S - first;
+      bulk_copy_s2cluster(map_to_rank(recv + rank * share * C::RLD, lane), smem_addr(part + first * C::RLD),
+                          (uint32_t)(n * C::RLD * 4), map_to_rank(&bars->received, lane));
     }
+  }
+  bool ok = true;
+  if (S > 1) {
+    ok = warp_wait(&bars->received, 0);
+    if (!ok && lane == 0) record_error(p.err, ERR_TIMEOUT, 68);
+    cluster_arrive();  // this CTA has all that was sent to it
   } else {
-    // Row m of the tile belongs to CTA r = ((m + 1) S - 1) / 128, which owns rows
-    // [128 r / S, 128 (r + 1) / S).  Receive buffer: [S][rows of the largest share][RLD].
-    float* recv = reinterpret_cast<float*>(smem);
-    const int share = (128 + S - 1) / S;
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();  // every CTA of the cluster has finished with its ring
-    if (warp >= 2) {
-      const int r = ((m + 1) * S - 1) / 128;
-      const uint32_t dst = map_to_rank(recv, r) + (uint32_t)(((rank * share + m - r * 128 / S) * C::RLD + col0) * 4);
-#pragma unroll
-      for (int c = 0; c < C::CW; c += 4) {
-        float v0, v1, v2, v3;
-        unpack2(acc[c / 2], v0, v1);
-        unpack2(acc[c / 2 + 1], v2, v3);
-        st_cluster_v4(dst + c * 4, v0, v1, v2, v3);
-      }
+    __syncthreads();
+    recv = part;
+  }
+  // ---- sums of this CTA's rows: a lane takes a row and four tokens
+  for (int g = warp; ok && g < (rows + 31) / 32 * (BN / 4); g += C::THREADS / 32) {
+    const int c = g % (BN / 4) * 4, m = g / (BN / 4) * 32 + lane;
+    if (m >= rows) continue;
+    float4 v = *reinterpret_cast<const float4*>(recv + m * C::RLD + c);
+    for (int r = 1; r < S; ++r) {
+      const float4 x = *reinterpret_cast<const float4*>(recv + (r * share + m) * C::RLD + c);
+      v.x += x.x;
+      v.y += x.y;
+      v.z += x.z;
+      v.w += x.w;
     }
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    const int lo = rank * 128 / S, rows = (rank + 1) * 128 / S - lo;
-    for (int e = threadIdx.x; e < rows * BN; e += C::THREADS) {
-      const int mr = e % rows, c = e / rows;
-      float v = 0.f;
-      for (int s = 0; s < S; ++s) v += recv[(s * share + mr) * C::RLD + c];
-      const int n = n0 + lo + mr;
-      const long t = t0 + c;
-      if (n < p.N && t < p.T) store_out(p, t, n, v);
+    const int n = n0 + lo + m;
+    const long t = t0 + c;
+    if (n < p.N) {
+      if (t < p.T) store_out(p, t, n, v.x);
+      if (t + 1 < p.T) store_out(p, t + 1, n, v.y);
+      if (t + 2 < p.T) store_out(p, t + 2, n, v.z);
+      if (t + 3 < p.T) store_out(p, t + 3, n, v.w);
     }
   }
   tc_fence_before();
@@ -353,6 +405,8 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
     tc_fence_after();
     tmem_dealloc(tmem, C::TCOLS);
   }
+  __syncwarp();
+  if (S > 1) cluster_wait();  // every CTA has received: no copy of this one's sums is under way
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -748,16 +802,49 @@ static bool map_bytes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of S CTAs of the kernel that the device holds at once (they do not span its GPCs, so it
+// is less than its SMs over S).  Looked up once per device and size.
+template <int BN>
+static int skinny_clusters(int S) {
+  using C = p8::SkCfg<BN>;
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][S].load(std::memory_order_relaxed);
+  if (n) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, p8::fp8_skinny_kernel<BN>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev][S].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 template <int BN>
 static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
   using C = p8::SkCfg<BN>;
   CUtensorMap mw, mx;
   if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN)) return kUnsupported;
   const int blocks = (a.K + 127) / 128, tiles_n = (a.N + 127) / 128;
-  const long tiles_t = (a.T + BN - 1) / BN;
+  const long tiles_t = (a.T + BN - 1) / BN, tiles = tiles_n * tiles_t;
   if (tiles_t > 65535 || tiles_n > 65535) return kUnsupported;
+  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // the most CTAs per tile that still run all at once, with two scale blocks each at least
   int S = 1;
-  while (S < 8 && tiles_n * tiles_t * (S + 1) <= 148 * C::OCC && (S + 1) * 2 <= blocks) ++S;
+  for (int s = 2; s <= 8 && 2 * s <= blocks; ++s)
+    if (tiles <= skinny_clusters<BN>(s)) S = s;
   p8::SkParams p;
   p.xs = a.xs;
   p.ws = a.ws;
@@ -769,8 +856,6 @@ static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
   p.out_ld = a.out_ld;
   p.out_f32 = a.act == MLA_F32;
   p.err = a.err;
-  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, (unsigned)tiles_t);
   cfg.blockDim = dim3(C::THREADS);
