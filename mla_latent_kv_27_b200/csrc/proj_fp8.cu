@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
                       const SkParams p) {
   using C = SkCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a cast of the rounded address: accesses stay shared-memory ones, not generic)
+  uint8_t* smem = smem_raw + ((1024u - smem_addr(smem_raw)) & 1023u);
   SkBars<BN>* bars = reinterpret_cast<SkBars<BN>*>(smem + C::BAR_OFF);
   float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -474,7 +475,8 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
                     const __grid_constant__ CUtensorMap tm_out, const WdParams p) {
   using C = WdCfg<WN>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a cast of the rounded address: accesses stay shared-memory ones, not generic)
+  uint8_t* smem = smem_raw + ((1024u - smem_addr(smem_raw)) & 1023u);
   WdBars<WN>* bars = reinterpret_cast<WdBars<WN>*>(smem + C::BAR_OFF);
   float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
