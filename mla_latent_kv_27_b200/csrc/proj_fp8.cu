@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "mla_internal.cuh"
 #include "proj_fp8.cuh"
@@ -700,9 +701,11 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < CH; ++j) {
 #pragma unroll
-            for (int c = 0; c < 32 && j * 32 + c < C::HC; ++c) {
-              const float s = blk0 + j * 32 + c / 16 * 16 < 128 ? s0 : s1;  // (rows of ws change at multiples of 16)
-              acc[j * 32 + c] = fmaf(__uint_as_float(j < C::NF ? v[j < C::NF ? j : 0][c] : vt[c % 16]), s, acc[j * 32 + c]);
+            for (int c = 0; c < 32 && j * 32 + c < C::HC; c += 2) {
+              const float sc = blk0 + j * 32 + c / 16 * 16 < 128 ? s0 : s1;  // (rows of ws change at multiples of 16)
+              const uint32_t* x = j < C::NF ? &v[j < C::NF ? j : 0][c] : &vt[c % 16];
+              float* to = acc + j * 32 + c;
+              unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), pack2(sc, sc), pack2(to[0], to[1])), to[0], to[1]);
             }
             // the next block's chunk takes the registers at once
             if (more) {
@@ -814,6 +817,8 @@ static int skinny_clusters(int S) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = known[dev][S].load(std::memory_order_relaxed);
   if (n) return n - 1;
+  if (cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S);
   cfg.blockDim = dim3(C::THREADS);
@@ -833,20 +838,27 @@ static int skinny_clusters(int S) {
   return n;
 }
 
+// CTAs per tile of the few-token kernel: the most that still run all at once, with two scale
+// blocks each at least.
+template <int BN>
+static int skinny_split(const Fp8Args& a) {
+  const int blocks = (a.K + 127) / 128;
+  const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
+  int S = 1;
+  for (int s = 2; s <= 8 && 2 * s <= blocks; ++s)
+    if (tiles <= skinny_clusters<BN>(s)) S = s;
+  return S;
+}
+
 template <int BN>
 static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
   using C = p8::SkCfg<BN>;
   CUtensorMap mw, mx;
   if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN)) return kUnsupported;
   const int blocks = (a.K + 127) / 128, tiles_n = (a.N + 127) / 128;
-  const long tiles_t = (a.T + BN - 1) / BN, tiles = tiles_n * tiles_t;
+  const long tiles_t = (a.T + BN - 1) / BN;
   if (tiles_t > 65535 || tiles_n > 65535) return kUnsupported;
-  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  // the most CTAs per tile that still run all at once, with two scale blocks each at least
-  int S = 1;
-  for (int s = 2; s <= 8 && 2 * s <= blocks; ++s)
-    if (tiles <= skinny_clusters<BN>(s)) S = s;
+  const int S = skinny_split<BN>(a);
   p8::SkParams p;
   p.xs = a.xs;
   p.ws = a.ws;
@@ -858,6 +870,8 @@ static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
   p.out_ld = a.out_ld;
   p.out_f32 = a.act == MLA_F32;
   p.err = a.err;
+  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, (unsigned)tiles_t);
   cfg.blockDim = dim3(C::THREADS);
@@ -958,13 +972,36 @@ static bool tma_layout(const Fp8Args& a) {
          a.x_ld % 16 == 0;
 }
 
+// Which kernel: up to 32 tokens the few-token one (the weights' bytes decide, and 16 or 32 columns keep
+// two CTAs on an SM).  Above, the variant with the least time by these models of what was measured on
+// B200 (us; a wave is one round of the CTAs or pairs that run at once):
+//   few tokens, 64 columns    waves (0.385 blocks per CTA + 4) + 1.5    64x7168x16384: 29 (many-token: 43)
+//   few tokens, 128 columns   waves (0.40 blocks per CTA + 7) + 1.5     128x7168x16384: 36 (64 columns: 50)
+//   many tokens, 128 outputs  waves (0.26 blocks + 0.75) + 4            256x7168x16384: 40 (few-token: 60)
+//   many tokens, 160 outputs  waves (0.307 blocks + 1.3) + 4            2048x7168x16384: 240 (128 outputs: 290)
+template <int BN>
+static float skinny_us(const Fp8Args& a, float block, float wave) {
+  const int blocks = (a.K + 127) / 128, S = skinny_split<BN>(a);
+  const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
+  const long waves = S > 1 ? 1 : (tiles + 147) / 148;
+  return waves * (block * ((blocks + S - 1) / S) + wave) + 1.5f;
+}
+static float wide_us(const Fp8Args& a, int wn, float block, float wave) {
+  const long tiles = (long)((a.N + wn - 1) / wn) * ((a.T + 255) / 256);
+  return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave) + 4.f;
+}
+
 cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
   if (!tma_layout(a)) return launch_fp8_any(a, st);
   if (a.T <= 16) return launch_skinny<16>(a, st);
   if (a.T <= 32) return launch_skinny<32>(a, st);
-  if (a.T <= 64) return launch_skinny<64>(a, st);
-  if (a.T <= 128) return launch_skinny<128>(a, st);
-  return launch_wide<160>(a, st);
+  const float w128 = wide_us(a, 128, 0.26f, 0.75f), w160 = wide_us(a, 160, 0.307f, 1.3f);
+  if (a.T <= 1024) {
+    const float s64 = skinny_us<64>(a, 0.385f, 4.f);
+    const float s128 = a.T > 64 ? skinny_us<128>(a, 0.40f, 7.f) : s64 + 1.f;
+    if (fminf(s64, s128) < fminf(w128, w160)) return s64 <= s128 ? launch_skinny<64>(a, st) : launch_skinny<128>(a, st);
+  }
+  return w128 < w160 ? launch_wide<128>(a, st) : launch_wide<160>(a, st);
 }
 
 }  // namespace mla
