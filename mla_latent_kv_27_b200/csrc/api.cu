@@ -302,8 +302,10 @@ mla_status mla_norm_rows(int32_t act_dtype, const void* x, int64_t x_ld, const v
   if (x_ld < width || (residual && residual_ld < width) || (sum_out && sum_ld < width) ||
       (y && y_ld < width) || (codes && codes_ld < width))
     return MLA_ERR_INVALID_ARG;
+  int* err = error_word_ptr();
+  if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, residual, residual_ld, gamma, n_tok, width, eps,
-                      sum_out, sum_ld, y, y_ld, codes, codes_ld, scales};
+                      sum_out, sum_ld, y, y_ld, codes, codes_ld, scales, err};
   return cuda_status(launch_rows(a, true, static_cast<cudaStream_t>(stream)));
 }
 
@@ -315,8 +317,10 @@ mla_status mla_quantize_rows(int32_t act_dtype, const void* x, int64_t x_ld, int
   if (n_tok < 0 || width <= 0) return MLA_ERR_INVALID_ARG;
   if (n_tok == 0) return MLA_OK;
   if (!x || !codes || !scales || x_ld < width || codes_ld < width) return MLA_ERR_INVALID_ARG;
+  int* err = error_word_ptr();
+  if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, nullptr, 0, nullptr, n_tok, width, 0.f,
-                      nullptr, 0, nullptr, 0, codes, codes_ld, scales};
+                      nullptr, 0, nullptr, 0, codes, codes_ld, scales, err};
   return cuda_status(launch_rows(a, false, static_cast<cudaStream_t>(stream)));
 }
 

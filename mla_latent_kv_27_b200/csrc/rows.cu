@@ -15,8 +15,7 @@
 namespace mla {
 namespace rows {
 
-using sm100::griddep_launch_dependents;
-using sm100::griddep_wait;
+using namespace sm100;
 
 // ------------------------------------------------------------------ helpers
 // max that keeps a NaN (fmaxf drops it), so a block that holds one gets a NaN scale
@@ -183,6 +182,111 @@ __global__ void __launch_bounds__(NT) rows_kernel(const RowsArgs a, int segments
         *reinterpret_cast<uint2*>(q + 8l * c) = codes8(v[i], inv);
         if (c % 16 == 0) sc[c / 16] = s;
       }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ norm of many rows
+// A CTA walks rows blockIdx, blockIdx + gridDim, ... with a ring of rows in shared memory that bulk
+// copies fill ahead of it, so loads are in flight through the barriers, sums and stores of a row (the
+// kernel above, a row per CTA, reached 4.1 TB/s on 8191 x 7168 with the residual; this one is noted
+// at its launch).  A stage holds a row of x and, after it, the residual's; it is refilled once
+// every thread has its values in registers, which the barrier of the row's sum shows.
+constexpr int RS_MAX_STAGES = 8;
+constexpr int RS_SMEM = 110 * 1024;
+constexpr int RS_ROWS = 600;
+
+template <typename T, int CH, int NT>
+__global__ void __launch_bounds__(NT) rows_stream_kernel(const RowsArgs a, int stages) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ uint64_t full[RS_MAX_STAGES];
+  __shared__ float part[2][32];  // alternating, so one barrier a row is enough
+  const uint32_t row_bytes = (uint32_t)a.width * sizeof(T);
+  const uint32_t stage_bytes = a.residual ? 2 * row_bytes : row_bytes;
+  const long stride = gridDim.x;
+  auto fetch = [&](long row, int s) {  // one thread
+    mbar_arrive_expect_tx(&full[s], stage_bytes);
+    uint8_t* st = ring + (size_t)s * stage_bytes;
+    bulk_load(st, static_cast<const T*>(a.x) + row * a.x_ld, row_bytes, &full[s]);
+    if (a.residual)
+      bulk_load(st + row_bytes, static_cast<const T*>(a.residual) + row * a.residual_ld, row_bytes, &full[s]);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  if (threadIdx.x == 0) {
+    griddep_launch_dependents();
+    for (int s = 0; s < stages; ++s)
+      if (blockIdx.x + s * stride < a.n_tok) fetch(blockIdx.x + s * stride, s);
+  }
+  const int chunks = a.width / 8;
+  const T* gamma = static_cast<const T*>(a.gamma);
+  float inv_width = 1.f / (float)a.width;
+  int s = 0;
+  uint32_t ph = 0, turn = 0;
+  for (long row = blockIdx.x; row < a.n_tok; row += stride, turn ^= 1) {
+    const bool landed = mbar_wait(&full[s], ph);
+    const T* x = reinterpret_cast<const T*>(ring + (size_t)s * stage_bytes);
+    float v[CH][8], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+      if (c < chunks) {
+        load8(x + 8 * c, v[i]);
+        if (a.residual) {
+          float r[8];
+          load8(x + a.width + 8 * c, r);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] += r[k];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss = fmaf(v[i][k], v[i][k], ss);
+    }
+    ss = warp_sum(ss);
+    if (threadIdx.x % 32 == 0) part[turn][threadIdx.x / 32] = ss;
+    if (!__syncthreads_and(landed ? 1 : 0)) {  // (all threads leave together)
+      if (threadIdx.x == 0) {
+        record_error(a.err, ERR_TIMEOUT, 70);
+        // the loads under way land (bounded) before the CTA's shared memory goes
+        for (int k = 0; k < stages && row + k * stride < a.n_tok; ++k)
+          mbar_wait(&full[(s + k) % stages], s + k < stages ? ph : ph ^ 1);
+      }
+      break;
+    }
+    if (threadIdx.x == 0 && row + stages * stride < a.n_tok) fetch(row + stages * stride, s);
+    const int lane = threadIdx.x % 32;
+    ss = warp_sum(lane < (int)blockDim.x / 32 ? part[turn][lane] : 0.f);
+    const float inv = __frsqrt_rn(ss * inv_width + a.eps);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      const bool in = c < chunks;
+      if (in) {
+        if (a.sum_out) store8(static_cast<T*>(a.sum_out) + row * a.sum_ld + 8 * c, v[i]);
+        float g[8];
+        if (gamma) load8(gamma + 8 * c, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = gamma ? v[i][k] * inv * g[k] : v[i][k] * inv;
+        if (a.y) store8(static_cast<T*>(a.y) + row * a.y_ld + 8 * c, v[i]);
+      }
+      if (a.codes) {
+        float sc, iv;
+        block_scale(amax_block(in ? amax8(v[i]) : 0.f), sc, iv);
+        if (in) {
+          *reinterpret_cast<uint2*>(a.codes + row * a.codes_ld + 8 * c) = codes8(v[i], iv);
+          if (c % 16 == 0) a.scales[row * ((a.width + 127) / 128) + c / 16] = sc;
+        }
+      }
+    }
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1;
     }
   }
 }
@@ -435,10 +539,11 @@ __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_any_kernel(const Ap
 // ------------------------------------------------------------------ host side
 // Launch with programmatic stream serialization (the kernels wait before they read anything).
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, Args... args) {
+static cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, int smem, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -465,20 +570,29 @@ template <typename T>
 static cudaError_t rows_impl(const RowsArgs& a, bool norm, cudaStream_t st) {
   using namespace rows;
   if (!rows_vector_ok<T>(a, norm)) {
-    return norm ? launch_pdl(rows_any_kernel<T, true>, (unsigned)a.n_tok, 256, st, a)
-                : launch_pdl(rows_any_kernel<T, false>, (unsigned)a.n_tok, 256, st, a);
+    return norm ? launch_pdl(rows_any_kernel<T, true>, (unsigned)a.n_tok, 256, st, 0, a)
+                : launch_pdl(rows_any_kernel<T, false>, (unsigned)a.n_tok, 256, st, 0, a);
   }
   const int chunks = a.width / 8;
   if (!norm) {
     const int nt = chunks >= 256 ? 256 : (chunks + 31) / 32 * 32;
     const long segments = (chunks + nt - 1) / nt;
     if (segments * a.n_tok > 0x7fffffffl) return kUnsupported;
-    return launch_pdl(rows_kernel<T, 1, 256, false>, (unsigned)(segments * a.n_tok), nt, st, a, (int)segments);
+    return launch_pdl(rows_kernel<T, 1, 256, false>, (unsigned)(segments * a.n_tok), nt, st, 0, a, (int)segments);
+  }
+  // many rows: persistent CTAs, two per SM, rows streamed through shared memory
+  const int row_bytes = a.width * (int)sizeof(T) * (a.residual ? 2 : 1);
+  const int stages = min(RS_MAX_STAGES, RS_SMEM / row_bytes);
+  if (a.n_tok >= RS_ROWS && stages >= 2 && chunks > 256 && chunks <= 1024) {
+    auto kernel = rows_stream_kernel<T, 2, 512>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RS_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, min(a.n_tok, 2 * 148), ((chunks + 1) / 2 + 31) / 32 * 32, st, stages * row_bytes, a, stages);
   }
   auto threads = [&](int ch) { return (unsigned)(((chunks + ch - 1) / ch + 31) / 32 * 32); };
-  if (chunks <= 256) return launch_pdl(rows_kernel<T, 1, 256, true>, (unsigned)a.n_tok, threads(1), st, a, 1);
-  if (chunks <= 1024) return launch_pdl(rows_kernel<T, 2, 512, true>, (unsigned)a.n_tok, threads(2), st, a, 1);
-  return launch_pdl(rows_kernel<T, 4, 1024, true>, (unsigned)a.n_tok, threads(4), st, a, 1);
+  if (chunks <= 256) return launch_pdl(rows_kernel<T, 1, 256, true>, (unsigned)a.n_tok, threads(1), st, 0, a, 1);
+  if (chunks <= 1024) return launch_pdl(rows_kernel<T, 2, 512, true>, (unsigned)a.n_tok, threads(2), st, 0, a, 1);
+  return launch_pdl(rows_kernel<T, 4, 1024, true>, (unsigned)a.n_tok, threads(4), st, 0, a, 1);
 }
 
 cudaError_t launch_rows(const RowsArgs& a, bool norm, cudaStream_t st) {
@@ -493,10 +607,10 @@ static cudaError_t append_rows_impl(const rows::AppendParams& p, cudaStream_t st
   const bool vec = p.d_c % 8 == 0 && p.d_rope % 8 == 0 && p.d_c <= 1024 && p.d_rope <= 256 && p.kv_ld % per16 == 0 &&
                    aligned(p.kv, 16) && aligned(p.gamma, 16) && aligned(p.rcos, 16) && aligned(p.rsin, 16) &&
                    aligned(p.cv.rows, 16) && (!FP8 || aligned(p.cv.rope, 16));
-  if (!vec) return launch_pdl(append_rows_any_kernel<T, FP8>, (unsigned)ctas, AR_WARPS * 32, st, p);
-  if (p.d_c <= 256) return launch_pdl(append_rows_kernel<T, 1, FP8>, (unsigned)ctas, AR_WARPS * 32, st, p);
-  if (p.d_c <= 512) return launch_pdl(append_rows_kernel<T, 2, FP8>, (unsigned)ctas, AR_WARPS * 32, st, p);
-  return launch_pdl(append_rows_kernel<T, 4, FP8>, (unsigned)ctas, AR_WARPS * 32, st, p);
+  if (!vec) return launch_pdl(append_rows_any_kernel<T, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
+  if (p.d_c <= 256) return launch_pdl(append_rows_kernel<T, 1, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
+  if (p.d_c <= 512) return launch_pdl(append_rows_kernel<T, 2, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
+  return launch_pdl(append_rows_kernel<T, 4, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
 }
 
 cudaError_t launch_append_rows(const mla_dims& d, const void* kv, int64_t kv_ld, int n_tok, const int32_t* seq_idx,

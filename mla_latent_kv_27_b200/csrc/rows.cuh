@@ -20,6 +20,7 @@ struct RowsArgs {
   uint8_t* codes;         // or null (then scales is null too)
   int64_t codes_ld;
   float* scales;          // [n_tok, ceil(width / 128)]
+  int* err;
 };
 
 // y = norm ? rmsnorm(x + residual) * gamma : x, written as act rows and / or as E4M3 blocks.
