@@ -35,49 +35,94 @@ __device__ __forceinline__ void block_scale(float amax, float& s, float& inv) {
   inv = amax == 0.f ? 1.f : __fdiv_rn(448.f, a);
 }
 
+// Eight consecutive values as four packed fp32 pairs: the adds, products and sums of squares then take
+// one instruction for two values (these kernels issue for half of their time at full bandwidth).
+struct Eight {
+  uint64_t p[4];
+};
+
 // two E4M3 codes (round to nearest even, saturating; NaN stays NaN), a in the low byte
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// eight consecutive values in 16-byte accesses
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+__device__ __forceinline__ Eight zero8() { return Eight{{0ull, 0ull, 0ull, 0ull}}; }
+// 16-byte accesses
+__device__ __forceinline__ Eight load8(const __nv_bfloat16* p) {
   const uint4 u = *reinterpret_cast<const uint4*>(p);
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  Eight v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) v.p[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return v;
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ Eight load8(const float* p) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0], b = reinterpret_cast<const ulonglong2*>(p)[1];
+  return Eight{{a.x, a.y, b.x, b.y}};
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Eight& v) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    float lo, hi;
+    unpack2(v.p[i], lo, hi);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float* p, const Eight& v) {
+  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(v.p[0], v.p[1]);
+  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(v.p[2], v.p[3]);
 }
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
-  uint2 q;
-  q.x = e4m3x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)) | (e4m3x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)) << 16);
-  q.y = e4m3x2(__fmul_rn(v[4], inv), __fmul_rn(v[5], inv)) | (e4m3x2(__fmul_rn(v[6], inv), __fmul_rn(v[7], inv)) << 16);
-  return q;
-}
-__device__ __forceinline__ float amax8(const float (&v)[8]) {
-  float m = fabsf(v[0]);
+__device__ __forceinline__ Eight add8(const Eight& a, const Eight& b) {
+  Eight r;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
+  for (int i = 0; i < 4; ++i) r.p[i] = add2(a.p[i], b.p[i]);
+  return r;
+}
+__device__ __forceinline__ Eight mul8(const Eight& a, const Eight& b) {
+  Eight r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = mul2(a.p[i], b.p[i]);
+  return r;
+}
+__device__ __forceinline__ Eight scale8(const Eight& a, float f) {
+  const uint64_t f2 = pack2(f, f);
+  Eight r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = mul2(a.p[i], f2);
+  return r;
+}
+// running sums of squares (even and odd values apart), and the pair's sum
+__device__ __forceinline__ void squares8(uint64_t& ss, const Eight& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ss = fma2(v.p[i], v.p[i], ss);
+}
+__device__ __forceinline__ float pair_sum(uint64_t ss) {
+  float lo, hi;
+  unpack2(ss, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ uint2 codes8(const Eight& v, float inv) {
+  const Eight x = scale8(v, inv);
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(x.p[i], lo, hi);
+    q[i] = e4m3x2(lo, hi);
+  }
+  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+__device__ __forceinline__ float amax8(const Eight& v) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(v.p[i], lo, hi);
+    m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
+  }
   return m;
 }
 // maximum over the 16 lanes that hold one block of 128 values
@@ -85,6 +130,27 @@ __device__ __forceinline__ float amax_block(float m) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
+}
+// Scales and reciprocals of CH blocks at once: lane i of each 16 divides for block i and the others get
+// its results (a division is some 20 instructions; a thread's CH blocks would take 2 CH of them).
+template <int CH>
+__device__ __forceinline__ void block_scales(const float (&amax)[CH], float (&s)[CH], float (&inv)[CH]) {
+  float mine = amax[0];
+#pragma unroll
+  for (int i = 1; i < CH; ++i)
+    if (threadIdx.x % 16 == i) mine = amax[i];
+  float ms, mi;
+  block_scale(mine, ms, mi);
+  if (CH == 1) {
+    s[0] = ms;
+    inv[0] = mi;
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      s[i] = __shfl_sync(0xffffffffu, ms, i, 16);
+      inv[i] = __shfl_sync(0xffffffffu, mi, i, 16);
+    }
+  }
 }
 
 // Sum over the CTA (whole warps), the same value in every thread; one barrier.
@@ -96,91 +162,210 @@ __device__ __forceinline__ float cta_sum(float v, float* part) {
   return warp_sum(lane < n ? part[lane] : 0.f);
 }
 
-// ------------------------------------------------------------------ norm / quantise, vector path
-// Thread i of a row's CTA holds chunks i, i + blockDim, ... of 8 values, CH of them, so 16
-// neighbouring lanes hold one 128-value block.  Without the norm a row is cut into segments
-// of blockDim * CH chunks, one CTA each (nothing crosses a block).
-template <typename T, int CH, int NT, bool NORM>
-__global__ void __launch_bounds__(NT) rows_kernel(const RowsArgs a, int segments) {
+// ------------------------------------------------------------------ quantise, vector path
+// A warp takes 512 values of a row, two chunks of 8 a lane (one chunk a lane reached 4.6 TB/s on
+// 4096 x 16384 bf16, two 6.1, four 5.7), so 16 neighbouring lanes hold one 128-value block.
+constexpr int RQ_WARPS = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(RQ_WARPS * 32) rows_quantize_kernel(const RowsArgs a, int units) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const unsigned unit = blockIdx.x * RQ_WARPS + threadIdx.x / 32;
+  const long row = unit / (unsigned)units;
+  if (row >= a.n_tok) return;
+  const int chunks = a.width / 8, c0 = (int)(unit % (unsigned)units) * 64 + lane;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
+  Eight v[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) v[i] = c0 + 32 * i < chunks ? load8(x + 8l * (c0 + 32 * i)) : zero8();
+  uint8_t* q = a.codes + row * a.codes_ld;
+  float* sc = a.scales + row * ((a.width + 127) / 128);
+  float m[2], s[2], inv[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) m[i] = amax_block(amax8(v[i]));
+  block_scales<2>(m, s, inv);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = c0 + 32 * i;
+    if (c < chunks) {
+      *reinterpret_cast<uint2*>(q + 8l * c) = codes8(v[i], inv[i]);
+      if (c % 16 == 0) sc[c / 16] = s[i];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ norm, vector path
+// One CTA per row: thread i holds chunks i, i + blockDim, ... of 8 values, CH of them, so 16
+// neighbouring lanes hold one 128-value block.
+template <typename T, int CH, int NT>
+__global__ void __launch_bounds__(NT) rows_kernel(const RowsArgs a) {
   __shared__ float part[32];
   griddep_wait();
   griddep_launch_dependents();
-  const long row = NORM ? blockIdx.x : blockIdx.x / segments;
-  const int seg = NORM ? 0 : (int)(blockIdx.x % segments);
-  const int chunks = a.width / 8;
-  const int c0 = seg * blockDim.x * CH + threadIdx.x;
+  const long row = blockIdx.x;
+  const int chunks = a.width / 8, c0 = threadIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
-  const T* res = NORM && a.residual ? static_cast<const T*>(a.residual) + row * a.residual_ld : nullptr;
-  const T* gamma = NORM ? static_cast<const T*>(a.gamma) : nullptr;
-  float v[CH][8], g[CH][8];
+  const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_ld : nullptr;
+  const T* gamma = static_cast<const T*>(a.gamma);
+  Eight v[CH], g[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = c0 + i * blockDim.x;
-    if (c < chunks)
-      load8(x + 8l * c, v[i]);
-    else
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+    v[i] = c < chunks ? load8(x + 8l * c) : zero8();
   }
-  if (NORM) {
-    if (res) {
+  if (res) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = c0 + i * blockDim.x;
-        if (c < chunks) {
-          float r[8];
-          load8(res + 8l * c, r);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][k] += r[k];
-        }
-      }
+    for (int i = 0; i < CH; ++i) {
+      const int c = c0 + i * blockDim.x;
+      if (c < chunks) v[i] = add8(v[i], load8(res + 8l * c));
     }
-    if (gamma) {
+  }
+  if (gamma) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = c0 + i * blockDim.x;
-        if (c < chunks) load8(gamma + 8l * c, g[i]);
-      }
+    for (int i = 0; i < CH; ++i) {
+      const int c = c0 + i * blockDim.x;
+      g[i] = c < chunks ? load8(gamma + 8l * c) : zero8();
     }
-    float ss = 0.f;
+  }
+  uint64_t sq = 0ull;
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
+  for (int i = 0; i < CH; ++i) squares8(sq, v[i]);
+  const float inv = __frsqrt_rn(cta_sum(pair_sum(sq), part) / (float)a.width + a.eps);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(v[i][k], v[i][k], ss);
-    const float inv = __frsqrt_rn(cta_sum(ss, part) / (float)a.width + a.eps);
-    if (a.sum_out) {
-      T* so = static_cast<T*>(a.sum_out) + row * a.sum_ld;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = c0 + i * blockDim.x;
-        if (c < chunks) store8(so + 8l * c, v[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = gamma ? v[i][k] * inv * g[i][k] : v[i][k] * inv;
-    if (a.y) {
-      T* y = static_cast<T*>(a.y) + row * a.y_ld;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = c0 + i * blockDim.x;
-        if (c < chunks) store8(y + 8l * c, v[i]);
-      }
-    }
+  for (int i = 0; i < CH; ++i) {
+    const int c = c0 + i * blockDim.x;
+    const bool in = c < chunks;
+    if (in && a.sum_out) store8(static_cast<T*>(a.sum_out) + row * a.sum_ld + 8l * c, v[i]);
+    v[i] = scale8(v[i], inv);
+    if (gamma) v[i] = mul8(v[i], g[i]);
+    if (in && a.y) store8(static_cast<T*>(a.y) + row * a.y_ld + 8l * c, v[i]);
   }
   if (a.codes) {
     uint8_t* q = a.codes + row * a.codes_ld;
     float* sc = a.scales + row * ((a.width + 127) / 128);
+    float m[CH], s[CH], iv[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) m[i] = amax_block(amax8(v[i]));
+    block_scales<CH>(m, s, iv);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = c0 + i * blockDim.x;
-      const bool in = c < chunks;
-      float s, inv;
-      block_scale(amax_block(in ? amax8(v[i]) : 0.f), s, inv);
+      if (c < chunks) {
+        *reinterpret_cast<uint2*>(q + 8l * c) = codes8(v[i], iv[i]);
+        if (c % 16 == 0) sc[c / 16] = s[i];
+      }
+    }
+  }
+}
+
+// Rows of at most 2048 values: a chunk a thread, and a CTA walks rows blockIdx, blockIdx + gridDim, ...
+// with the next row's loads under way (a row per CTA left 16384 x 1536 at 2.7 TB/s: its CTAs come
+// and go faster than they are launched).
+template <typename T>
+struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) rows_loop_kernel(const RowsArgs a) {
+  __shared__ float part[2][32];  // alternating, so one barrier a row is enough
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = threadIdx.x, lane = threadIdx.x % 32;
+  const bool in = c < a.width / 8;
+  const T* x = static_cast<const T*>(a.x) + 8 * c;
+  const T* res = static_cast<const T*>(a.residual) + 8 * c;
+  const Eight g = in && a.gamma ? load8(static_cast<const T*>(a.gamma) + 8 * c) : zero8();
+  Raw8<T> nx = {}, nr = {};
+  long row = blockIdx.x;
+  if (in) {
+    nx = raw8(x + row * a.x_ld);
+    if (a.residual) nr = raw8(res + row * a.residual_ld);
+  }
+  for (int turn = 0; row < a.n_tok; row += gridDim.x, turn ^= 1) {
+    Eight v = zero8();
+    if (in) {
+      v = load8(reinterpret_cast<const T*>(&nx));
+      if (a.residual) v = add8(v, load8(reinterpret_cast<const T*>(&nr)));
+    }
+    const long next = row + gridDim.x;
+    if (in && next < a.n_tok) {
+      nx = raw8(x + next * a.x_ld);
+      if (a.residual) nr = raw8(res + next * a.residual_ld);
+    }
+    uint64_t sq = 0ull;
+    squares8(sq, v);
+    const float ss = warp_sum(pair_sum(sq));
+    if (lane == 0) part[turn][threadIdx.x / 32] = ss;
+    __syncthreads();
+    const float inv =
+        __frsqrt_rn(warp_sum(lane < (int)blockDim.x / 32 ? part[turn][lane] : 0.f) / (float)a.width + a.eps);
+    if (in && a.sum_out) store8(static_cast<T*>(a.sum_out) + row * a.sum_ld + 8 * c, v);
+    v = scale8(v, inv);
+    if (a.gamma) v = mul8(v, g);
+    if (in && a.y) store8(static_cast<T*>(a.y) + row * a.y_ld + 8 * c, v);
+    if (a.codes) {
+      float s, iv;
+      block_scale(amax_block(amax8(v)), s, iv);
       if (in) {
-        *reinterpret_cast<uint2*>(q + 8l * c) = codes8(v[i], inv);
-        if (c % 16 == 0) sc[c / 16] = s;
+        *reinterpret_cast<uint2*>(a.codes + row * a.codes_ld + 8 * c) = codes8(v, iv);
+        if (c % 16 == 0) a.scales[row * ((a.width + 127) / 128) + c / 16] = s;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ norm of narrow rows
+// One warp per row, CH chunks of 8 values a lane, no barrier.
+constexpr int RW_WARPS = 4;
+
+template <typename T, int CH>
+__global__ void __launch_bounds__(RW_WARPS * 32) rows_warp_kernel(const RowsArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const long row = (long)blockIdx.x * RW_WARPS + threadIdx.x / 32;
+  if (row >= a.n_tok) return;
+  const int chunks = a.width / 8;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
+  const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_ld : nullptr;
+  const T* gamma = static_cast<const T*>(a.gamma);
+  Eight v[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) v[i] = lane + 32 * i < chunks ? load8(x + 8 * (lane + 32 * i)) : zero8();
+  uint64_t sq = 0ull;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = lane + 32 * i;
+    if (res && c < chunks) v[i] = add8(v[i], load8(res + 8 * c));
+    squares8(sq, v[i]);
+  }
+  const float inv = __frsqrt_rn(warp_sum(pair_sum(sq)) / (float)a.width + a.eps);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = lane + 32 * i;
+    const bool in = c < chunks;
+    if (in) {
+      if (a.sum_out) store8(static_cast<T*>(a.sum_out) + row * a.sum_ld + 8 * c, v[i]);
+      v[i] = scale8(v[i], inv);
+      if (gamma) v[i] = mul8(v[i], load8(gamma + 8 * c));
+      if (a.y) store8(static_cast<T*>(a.y) + row * a.y_ld + 8 * c, v[i]);
+    }
+    if (a.codes) {
+      float s, iv;
+      block_scale(amax_block(amax8(v[i])), s, iv);
+      if (in) {
+        *reinterpret_cast<uint2*>(a.codes + row * a.codes_ld + 8 * c) = codes8(v[i], iv);
+        if (c % 16 == 0) a.scales[row * ((a.width + 127) / 128) + c / 16] = s;
       }
     }
   }
@@ -195,9 +380,10 @@ __global__ void __launch_bounds__(NT) rows_kernel(const RowsArgs a, int segments
 constexpr int RS_MAX_STAGES = 8;
 constexpr int RS_SMEM = 110 * 1024;
 constexpr int RS_ROWS = 600;
+constexpr int LOOP_THREADS = 1024;
 
 template <typename T, int CH, int NT>
-__global__ void __launch_bounds__(NT) rows_stream_kernel(const RowsArgs a, int stages) {
+__global__ void __launch_bounds__(NT) rows_stream_kernel(const RowsArgs a, int stages, int gamma_staged) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ uint64_t full[RS_MAX_STAGES];
   __shared__ float part[2][32];  // alternating, so one barrier a row is enough
@@ -223,31 +409,37 @@ __global__ void __launch_bounds__(NT) rows_stream_kernel(const RowsArgs a, int s
       if (blockIdx.x + s * stride < a.n_tok) fetch(blockIdx.x + s * stride, s);
   }
   const int chunks = a.width / 8;
+  const float inv_width = 1.f / (float)a.width;
+  // The weight is kept in shared memory (the L1 left beside the ring does not hold it), except where
+  // the sum and the normed rows are both written: there, read from L2 for each row, it was the faster
+  // (8191 x 7168 with the residual: 87 us against 98; with 8-bit rows and the sum alone 73 against 69).
   const T* gamma = static_cast<const T*>(a.gamma);
-  float inv_width = 1.f / (float)a.width;
+  if (gamma_staged) {
+    gamma = reinterpret_cast<const T*>(ring + (size_t)stages * stage_bytes);
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x)
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+        reinterpret_cast<uint4*>(ring + (size_t)stages * stage_bytes)[c * (sizeof(T) / 2) + k] =
+            static_cast<const uint4*>(a.gamma)[c * (sizeof(T) / 2) + k];
+  }
   int s = 0;
   uint32_t ph = 0, turn = 0;
   for (long row = blockIdx.x; row < a.n_tok; row += stride, turn ^= 1) {
     const bool landed = mbar_wait(&full[s], ph);
     const T* x = reinterpret_cast<const T*>(ring + (size_t)s * stage_bytes);
-    float v[CH][8], ss = 0.f;
+    Eight v[CH];
+    uint64_t sq = 0ull;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+      v[i] = zero8();
       if (c < chunks) {
-        load8(x + 8 * c, v[i]);
-        if (a.residual) {
-          float r[8];
-          load8(x + a.width + 8 * c, r);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][k] += r[k];
-        }
+        v[i] = load8(x + 8 * c);
+        if (a.residual) v[i] = add8(v[i], load8(x + a.width + 8 * c));
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(v[i][k], v[i][k], ss);
+      squares8(sq, v[i]);
     }
+    float ss = pair_sum(sq);
     ss = warp_sum(ss);
     if (threadIdx.x % 32 == 0) part[turn][threadIdx.x / 32] = ss;
     if (!__syncthreads_and(landed ? 1 : 0)) {  // (all threads leave together)
@@ -266,19 +458,16 @@ __global__ void __launch_bounds__(NT) rows_stream_kernel(const RowsArgs a, int s
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      const bool in = c < chunks;
-      if (in) {
+      if (c < chunks) {
         if (a.sum_out) store8(static_cast<T*>(a.sum_out) + row * a.sum_ld + 8 * c, v[i]);
-        float g[8];
-        if (gamma) load8(gamma + 8 * c, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = gamma ? v[i][k] * inv * g[k] : v[i][k] * inv;
+        v[i] = scale8(v[i], inv);
+        if (gamma) v[i] = mul8(v[i], load8(gamma + 8 * c));
         if (a.y) store8(static_cast<T*>(a.y) + row * a.y_ld + 8 * c, v[i]);
       }
       if (a.codes) {
         float sc, iv;
-        block_scale(amax_block(in ? amax8(v[i]) : 0.f), sc, iv);
-        if (in) {
+        block_scale(amax_block(amax8(v[i])), sc, iv);
+        if (c < chunks) {
           *reinterpret_cast<uint2*>(a.codes + row * a.codes_ld + 8 * c) = codes8(v[i], iv);
           if (c % 16 == 0) a.scales[row * ((a.width + 127) / 128) + c / 16] = sc;
         }
@@ -359,113 +548,145 @@ struct AppendParams {
   const float* rcos;
   const float* rsin;
   int rope_rows;
+  int page_shift;  // log2 of page_size, or -1 when it is no power of two (a division is some 30 instructions)
   CacheView cv;
   int* err;
 };
 
-// Slot (page * page_size + offset) of token t, or -1 with the error recorded (by one lane).
-__device__ __forceinline__ long slot_of(const AppendParams& p, int t, int& ps, bool report) {
-  const int seq = p.seq_idx[t];
-  ps = p.pos[t];
-  if (seq < 0 || seq >= p.cv.num_seqs) {
-    if (report) record_error(p.err, ERR_SEQ, seq);
-    return -1;
-  }
-  if (ps < 0 || ps >= p.rope_rows || ps / p.cv.page_size >= p.cv.max_pages) {
-    if (report) record_error(p.err, ERR_POS, ps);
-    return -1;
-  }
-  const int pid = p.cv.block_table[(long)seq * p.cv.max_pages + ps / p.cv.page_size];
-  if (pid < 0 || pid >= p.cv.num_pages) {
-    if (report) record_error(p.err, ERR_PAGE, pid);
-    return -1;
-  }
-  return (long)pid * p.cv.page_size + ps % p.cv.page_size;
+__device__ __forceinline__ int page_of(const AppendParams& p, int pos) {
+  return p.page_shift >= 0 ? pos >> p.page_shift : pos / p.cv.page_size;
+}
+
+// Where a token goes: its page id (or what is wrong with it: PLACE_SEQ, PLACE_POS; an id outside the
+// cache stays as it was read) and position.
+constexpr int PLACE_SEQ = -0x7fffffff, PLACE_POS = PLACE_SEQ + 1;
+struct Place {
+  int seq, pos, pid;
+  int row;  // of the page
+};
+__device__ __forceinline__ Place place_of(const AppendParams& p, int seq, int pos) {
+  Place r = {seq, pos, PLACE_SEQ, 0};
+  if (seq < 0 || seq >= p.cv.num_seqs) return r;
+  r.pid = PLACE_POS;
+  if (pos < 0 || pos >= p.rope_rows) return r;
+  const int page = page_of(p, pos);
+  if (page >= p.cv.max_pages) return r;
+  r.row = pos - page * p.cv.page_size;
+  r.pid = p.cv.block_table[(long)seq * p.cv.max_pages + page];
+  return r;
+}
+// records why a token is skipped
+__device__ __forceinline__ void report(const AppendParams& p, const Place& r) {
+  if (r.pid == PLACE_SEQ && (r.seq < 0 || r.seq >= p.cv.num_seqs))
+    record_error(p.err, ERR_SEQ, r.seq);
+  else if (r.pid == PLACE_POS && (r.pos < 0 || r.pos >= p.rope_rows || page_of(p, r.pos) >= p.cv.max_pages))
+    record_error(p.err, ERR_POS, r.pos);
+  else
+    record_error(p.err, ERR_PAGE, r.pid);
 }
 
 constexpr int AR_WARPS = 4;
 
 // One warp per token: lane l holds chunks l, l + 32, ... of 8 latent values (CH of them, 16 lanes a
-// 128-value block) and, below d_rope / 8 lanes, one chunk of the rotary key.
+// 128-value block) and, below d_rope / 8 lanes, one chunk of the rotary key.  A warp walks tokens w,
+// w + (warps of the grid), ... with the next token's row and its page id (whose position came one
+// token earlier still) under way; a token a warp waited for each of these in turn.
 template <typename T, int CH, bool FP8>
 __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
-  const long t = (long)blockIdx.x * AR_WARPS + threadIdx.x / 32;
-  if (t >= p.T) return;
-  const T* src = static_cast<const T*>(p.kv) + t * p.kv_ld;
+  const long stride = (long)gridDim.x * AR_WARPS;
   const T* gamma = static_cast<const T*>(p.gamma);
   const int chunks = p.d_c / 8;
   const bool rot = lane < p.d_rope / 8;
-  float v[CH][8], g[CH][8], k[8];
+  Raw8<T> g[CH], nv[CH], nk = {};
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = lane + 32 * i;
-    if (c < chunks)
-      load8(src + 8 * c, v[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    g[i] = {};
+    nv[i] = {};
+    if (gamma && lane + 32 * i < chunks) g[i] = raw8(gamma + 8 * (lane + 32 * i));
   }
-  if (rot) load8(src + p.d_c + 8 * lane, k);
-  if (gamma) {
+  long t = (long)blockIdx.x * AR_WARPS + threadIdx.x / 32;
+  auto fetch = [&](long t) {
+    const T* src = static_cast<const T*>(p.kv) + t * p.kv_ld;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = lane + 32 * i;
-      if (c < chunks) load8(gamma + 8 * c, g[i]);
+    for (int i = 0; i < CH; ++i)
+      if (lane + 32 * i < chunks) nv[i] = raw8(src + 8 * (lane + 32 * i));
+    if (rot) nk = raw8(src + p.d_c + 8 * lane);
+  };
+  int seq = 0, ps = 0;    // of the token after the current one
+  auto where = [&](long t) {
+    seq = p.seq_idx[t];
+    ps = p.pos[t];
+  };
+  if (t >= p.T) return;
+  where(t);
+  fetch(t);
+  Place here = place_of(p, seq, ps);
+  if (t + stride < p.T) where(t + stride);
+  for (; t < p.T; t += stride) {
+    Eight v[CH], k = load8(reinterpret_cast<const T*>(&nk));
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = load8(reinterpret_cast<const T*>(&nv[i]));
+    const Place now = here;
+    const bool ok = now.pid >= 0 && now.pid < p.cv.num_pages;
+    float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (rot && ok) {
+      const long at = (long)now.pos * (p.d_rope / 2) + 4 * lane;
+      cs = *reinterpret_cast<const float4*>(p.rcos + at);
+      sn = *reinterpret_cast<const float4*>(p.rsin + at);
     }
-  }
-  int ps;
-  const long slot = slot_of(p, (int)t, ps, lane == 0);
-  if (slot < 0) return;
-  if (rot) {
-    const long at = (long)ps * (p.d_rope / 2) + 4 * lane;
-    const float4 cs = *reinterpret_cast<const float4*>(p.rcos + at);
-    const float4 sn = *reinterpret_cast<const float4*>(p.rsin + at);
+    if (t + stride < p.T) {
+      fetch(t + stride);
+      here = place_of(p, seq, ps);
+      if (t + 2 * stride < p.T) where(t + 2 * stride);
+    }
+    if (!ok) {
+      if (lane == 0) report(p, now);
+      continue;
+    }
+    const long slot = (long)now.pid * p.cv.page_size + now.row;
+    if (gamma) {
+      uint64_t sq = 0ull;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) squares8(sq, v[i]);
+      const float inv = __frsqrt_rn(warp_sum(pair_sum(sq)) / (float)p.d_c + p.eps);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) v[i] = mul8(scale8(v[i], inv), load8(reinterpret_cast<const T*>(&g[i])));
+    }
     const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float a = k[2 * j], b = k[2 * j + 1];
-      k[2 * j] = a * cc[j] - b * ss[j];
-      k[2 * j + 1] = a * ss[j] + b * cc[j];
+      float a, b;
+      unpack2(k.p[j], a, b);
+      k.p[j] = pack2(a * cc[j] - b * ss[j], a * ss[j] + b * cc[j]);
     }
-  }
-  if (gamma) {
-    float sq = 0.f;
+    if (FP8) {
+      uint8_t* q = static_cast<uint8_t*>(p.cv.rows) + slot * p.d_c;
+      float* sc = p.cv.scales + slot * (p.d_c / 128);
+      float m[CH], s[CH], inv[CH];
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
+      for (int i = 0; i < CH; ++i) m[i] = amax_block(amax8(v[i]));
+      block_scales<CH>(m, s, inv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(v[i][j], v[i][j], sq);
-    const float inv = __frsqrt_rn(warp_sum(sq) / (float)p.d_c + p.eps);
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * g[i][j];
-  }
-  if (FP8) {
-    uint8_t* q = static_cast<uint8_t*>(p.cv.rows) + slot * p.d_c;
-    float* sc = p.cv.scales + slot * (p.d_c / 128);
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = lane + 32 * i;
-      const bool in = c < chunks;
-      float s, inv;
-      block_scale(amax_block(in ? amax8(v[i]) : 0.f), s, inv);
-      if (in) {
-        *reinterpret_cast<uint2*>(q + 8 * c) = codes8(v[i], inv);
-        if (c % 16 == 0) sc[c / 16] = s;
+      for (int i = 0; i < CH; ++i) {
+        const int c = lane + 32 * i;
+        if (c < chunks) {
+          *reinterpret_cast<uint2*>(q + 8 * c) = codes8(v[i], inv[i]);
+          if (c % 16 == 0) sc[c / 16] = s[i];
+        }
       }
-    }
-    if (rot) store8(static_cast<__nv_bfloat16*>(p.cv.rope) + slot * p.d_rope + 8 * lane, k);
-  } else {
-    T* row = static_cast<T*>(p.cv.rows) + slot * (p.d_c + p.d_rope);
+      if (rot) store8(static_cast<__nv_bfloat16*>(p.cv.rope) + slot * p.d_rope + 8 * lane, k);
+    } else {
+      T* row = static_cast<T*>(p.cv.rows) + slot * (p.d_c + p.d_rope);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = lane + 32 * i;
-      if (c < chunks) store8(row + 8 * c, v[i]);
+      for (int i = 0; i < CH; ++i) {
+        const int c = lane + 32 * i;
+        if (c < chunks) store8(row + 8 * c, v[i]);
+      }
+      if (rot) store8(row + p.d_c + 8 * lane, k);
     }
-    if (rot) store8(row + p.d_c + 8 * lane, k);
   }
 }
 
@@ -480,9 +701,13 @@ __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_any_kernel(const Ap
   if (t >= p.T) return;
   const T* src = static_cast<const T*>(p.kv) + t * p.kv_ld;
   const T* gamma = static_cast<const T*>(p.gamma);
-  int ps;
-  const long slot = slot_of(p, (int)t, ps, lane == 0);
-  if (slot < 0) return;
+  const Place at = place_of(p, p.seq_idx[t], p.pos[t]);
+  if (at.pid < 0 || at.pid >= p.cv.num_pages) {
+    if (lane == 0) report(p, at);
+    return;
+  }
+  const int ps = at.pos;
+  const long slot = (long)at.pid * p.cv.page_size + at.row;
   float inv = 1.f;
   if (gamma) {
     float sq = 0.f;
@@ -575,24 +800,27 @@ static cudaError_t rows_impl(const RowsArgs& a, bool norm, cudaStream_t st) {
   }
   const int chunks = a.width / 8;
   if (!norm) {
-    const int nt = chunks >= 256 ? 256 : (chunks + 31) / 32 * 32;
-    const long segments = (chunks + nt - 1) / nt;
-    if (segments * a.n_tok > 0x7fffffffl) return kUnsupported;
-    return launch_pdl(rows_kernel<T, 1, 256, false>, (unsigned)(segments * a.n_tok), nt, st, 0, a, (int)segments);
+    const int units = (chunks + 63) / 64;
+    const long ctas = ((long)units * a.n_tok + RQ_WARPS - 1) / RQ_WARPS;
+    if (ctas * RQ_WARPS > 0x7fffffffl) return kUnsupported;
+    return launch_pdl(rows_quantize_kernel<T>, (unsigned)ctas, RQ_WARPS * 32, st, 0, a, units);
   }
+  if (chunks <= 64)
+    return launch_pdl(rows_warp_kernel<T, 2>, ((unsigned)a.n_tok + RW_WARPS - 1) / RW_WARPS, RW_WARPS * 32, st, 0, a);
   // many rows: persistent CTAs, two per SM, rows streamed through shared memory
-  const int row_bytes = a.width * (int)sizeof(T) * (a.residual ? 2 : 1);
-  const int stages = min(RS_MAX_STAGES, RS_SMEM / row_bytes);
+  const int one = a.width * (int)sizeof(T), row_bytes = a.residual ? 2 * one : one, fixed = a.gamma && !(a.sum_out && a.y) ? one : 0;
+  const int stages = min(RS_MAX_STAGES, (RS_SMEM - fixed) / row_bytes);
   if (a.n_tok >= RS_ROWS && stages >= 2 && chunks > 256 && chunks <= 1024) {
     auto kernel = rows_stream_kernel<T, 2, 512>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RS_SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, min(a.n_tok, 2 * 148), ((chunks + 1) / 2 + 31) / 32 * 32, st, stages * row_bytes, a, stages);
+    return launch_pdl(kernel, min(a.n_tok, 2 * 148), ((chunks + 1) / 2 + 31) / 32 * 32, st, stages * row_bytes + fixed, a, stages, fixed > 0 ? 1 : 0);
   }
   auto threads = [&](int ch) { return (unsigned)(((chunks + ch - 1) / ch + 31) / 32 * 32); };
-  if (chunks <= 256) return launch_pdl(rows_kernel<T, 1, 256, true>, (unsigned)a.n_tok, threads(1), st, 0, a, 1);
-  if (chunks <= 1024) return launch_pdl(rows_kernel<T, 2, 512, true>, (unsigned)a.n_tok, threads(2), st, 0, a, 1);
-  return launch_pdl(rows_kernel<T, 4, 1024, true>, (unsigned)a.n_tok, threads(4), st, 0, a, 1);
+  if (chunks <= 256)
+    return launch_pdl(rows_loop_kernel<T>, min(a.n_tok, 148 * (LOOP_THREADS / (int)threads(1))), threads(1), st, 0, a);
+  if (chunks <= 1024) return launch_pdl(rows_kernel<T, 2, 512>, (unsigned)a.n_tok, threads(2), st, 0, a);
+  return launch_pdl(rows_kernel<T, 4, 1024>, (unsigned)a.n_tok, threads(4), st, 0, a);
 }
 
 cudaError_t launch_rows(const RowsArgs& a, bool norm, cudaStream_t st) {
@@ -608,9 +836,11 @@ static cudaError_t append_rows_impl(const rows::AppendParams& p, cudaStream_t st
                    aligned(p.kv, 16) && aligned(p.gamma, 16) && aligned(p.rcos, 16) && aligned(p.rsin, 16) &&
                    aligned(p.cv.rows, 16) && (!FP8 || aligned(p.cv.rope, 16));
   if (!vec) return launch_pdl(append_rows_any_kernel<T, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
-  if (p.d_c <= 256) return launch_pdl(append_rows_kernel<T, 1, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
-  if (p.d_c <= 512) return launch_pdl(append_rows_kernel<T, 2, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
-  return launch_pdl(append_rows_kernel<T, 4, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
+  const long at_once = 148 * (sizeof(T) == 4 ? 4 : 5);  // what the registers of d_c = 512 (116 and 96) let run at once
+  const unsigned grid = (unsigned)(ctas < at_once ? ctas : at_once);
+  if (p.d_c <= 256) return launch_pdl(append_rows_kernel<T, 1, FP8>, grid, AR_WARPS * 32, st, 0, p);
+  if (p.d_c <= 512) return launch_pdl(append_rows_kernel<T, 2, FP8>, grid, AR_WARPS * 32, st, 0, p);
+  return launch_pdl(append_rows_kernel<T, 4, FP8>, grid, AR_WARPS * 32, st, 0, p);
 }
 
 cudaError_t launch_append_rows(const mla_dims& d, const void* kv, int64_t kv_ld, int n_tok, const int32_t* seq_idx,
@@ -629,6 +859,9 @@ cudaError_t launch_append_rows(const mla_dims& d, const void* kv, int64_t kv_ld,
   p.rcos = rcos;
   p.rsin = rsin;
   p.rope_rows = rope_rows;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (cv.page_size == 1 << s) p.page_shift = s;
   p.cv = cv;
   p.err = err;
   if (d.act_dtype == MLA_F32) return append_rows_impl<float, false>(p, st);

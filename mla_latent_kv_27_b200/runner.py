@@ -9,6 +9,9 @@ a decode step as four library calls on one stream:
     mla_decode_attention split-KV attention + log-sum-exp combine  (steps 3, 4)
     mla_output_up        out = W_UV o_lat                          (step 5)
 
+``MLALayer`` adds what a whole attention layer has around these: the norms, the 8-bit projections
+down to the latents and up to the queries, and the 8-bit output projection (see its docstring).
+
 Sequence b holds L_b tokens after the step: L_b - S_q cached before it, and the S_q new
 tokens at positions L_b - S_q .. L_b - 1, whose queries attend causally when S_q > 1.
 """
@@ -289,3 +292,89 @@ class MLARunner:
             B.mla_output_up(self.dims, self.o_lat, self.n_tok, self.w_uv, out, compute)
         drain(n - 1)
         compute.wait_event(drained[(n - 1) % 2])
+
+
+E4M3_MAX = 448.0
+BLOCK = 128  # values that share a scale
+
+
+def quantize_weight(w: torch.Tensor):
+    """8-bit form of a weight [n, k]: E4M3 codes (uint8 [n, k]) and one fp32 scale per 128 x 128 block,
+    amax / 448 (1 for an all-zero block), as mla_project_fp8 takes them.  Done once per weight."""
+    n, k = w.shape
+    nb, kb = -(-n // BLOCK), -(-k // BLOCK)
+    blocks = torch.nn.functional.pad(w.float(), (0, kb * BLOCK - k, 0, nb * BLOCK - n)).view(nb, BLOCK, kb, BLOCK)
+    amax = blocks.abs().amax((1, 3))
+    scales = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))
+    codes = (blocks / scales[:, None, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+    codes = codes.view(nb * BLOCK, kb * BLOCK)[:n, :k].contiguous().view(torch.uint8)
+    return codes, scales.contiguous()
+
+
+class MLALayer(MLARunner):
+    """A whole MLA layer's decode step, with 8-bit projections around the attention core:
+
+        mla_norm_rows        r = x + residual, its norm as 8-bit rows
+        mla_project_fp8      [q_rank | d_c | d_rope] = W_down r
+        mla_append_rows      the latent normed, the rotary key rotated -> cache
+        mla_norm_rows        the query latent's norm as 8-bit rows
+        mla_project_fp8 x 2  q_nope and q_rope of all heads
+        mla_absorb_query, mla_decode_attention, mla_output_up
+        mla_quantize_rows    the heads' outputs as 8-bit rows
+        mla_project_fp8      y = W_O out
+
+    ``h_new`` and ``residual`` are the step's inputs ([tokens, d_model]); ``layer_step`` returns y
+    ([tokens, d_model], the layer's output) and leaves the sum r in ``residual``.  The weights are drawn
+    N(0, 1/fan_in) and quantised once; the norms' weights are drawn around 1."""
+
+    def __init__(self, w: wl.Workload, q_rank: int, eps: float = 1e-6, **kw):
+        super().__init__(w, **kw)
+        self.q_rank, self.eps = q_rank, eps
+        dev, dt, T = self.device, _TORCH[w.act_dtype], self.n_tok
+        self.act = _ACT[w.act_dtype]
+        gen = torch.Generator(device=dev)
+        gen.manual_seed(5000 + 17 * w.seed)
+
+        def weight(n, k):
+            return quantize_weight(torch.randn((n, k), generator=gen, device=dev) / k ** 0.5)
+
+        def gamma(n):
+            return (1 + 0.1 * torch.randn(n, generator=gen, device=dev)).to(dt)
+
+        self.d_down = q_rank + w.row_width
+        self.w_down, self.s_down = weight(self.d_down, w.d_model)
+        self.w_qn, self.s_qn = weight(w.n_heads * w.d_nope, q_rank)
+        self.w_qr, self.s_qr = weight(w.n_heads * w.d_rope, q_rank)
+        self.w_o, self.s_o = weight(w.d_model, w.n_heads * w.d_v)
+        self.g_in, self.g_q, self.g_kv = gamma(w.d_model), gamma(q_rank), gamma(w.d_c)
+        rows = lambda n: (torch.empty((T, n), dtype=torch.uint8, device=dev),  # noqa: E731
+                          torch.empty((T, -(-n // BLOCK)), dtype=torch.float32, device=dev))
+        self.x8, self.x8_s = rows(w.d_model)
+        self.q8, self.q8_s = rows(q_rank)
+        self.o8, self.o8_s = rows(w.n_heads * w.d_v)
+        self.residual = torch.zeros((T, w.d_model), dtype=dt, device=dev)
+        self.down = torch.empty((T, self.d_down), dtype=dt, device=dev)
+        self.y = torch.empty((T, w.d_model), dtype=dt, device=dev)
+
+    def layer_step(self, stream=None):
+        w, T, st = self.w, self.n_tok, stream or self.stream
+        D, R, HV = w.d_model, self.q_rank, w.n_heads * w.d_v
+        B.mla_norm_rows(self.act, self.h_new, D, self.residual, D, self.g_in, T, D, self.eps, self.residual, D,
+                        None, 0, self.x8, D, self.x8_s, st)
+        B.mla_project_fp8(self.act, self.x8, D, self.x8_s, T, self.w_down, self.s_down, self.d_down, D, self.down,
+                          self.d_down, st)
+        B.mla_append_rows(self.dims, self.down[:, R:], self.d_down, T, self.seq_idx, self.pos, self.g_kv, self.eps,
+                          self.rope_cos, self.rope_sin, self.rope_rows, self.cache.desc, st)
+        B.mla_norm_rows(self.act, self.down, self.d_down, None, 0, self.g_q, T, R, self.eps, None, 0, None, 0,
+                        self.q8, R, self.q8_s, st)
+        # q_nope first: the absorb reads it before the call in front of it (q_rope's) has completed
+        B.mla_project_fp8(self.act, self.q8, R, self.q8_s, T, self.w_qn, self.s_qn, w.n_heads * w.d_nope, R,
+                          self.q_nope, w.n_heads * w.d_nope, st)
+        B.mla_project_fp8(self.act, self.q8, R, self.q8_s, T, self.w_qr, self.s_qr, w.n_heads * w.d_rope, R,
+                          self.q_rope, w.n_heads * w.d_rope, st)
+        self.absorb(st)
+        self.decode(st)
+        self.output(st)
+        B.mla_quantize_rows(self.act, self.out, HV, T, HV, self.o8, HV, self.o8_s, st)
+        B.mla_project_fp8(self.act, self.o8, HV, self.o8_s, T, self.w_o, self.s_o, D, HV, self.y, D, st)
+        return self.y
