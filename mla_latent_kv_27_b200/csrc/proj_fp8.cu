@@ -139,7 +139,9 @@ __device__ __forceinline__ void store_out(const SkParams& p, long t, int n, floa
   else
     static_cast<__nv_bfloat16*>(p.out)[t * p.out_ld + n] = __float2bfloat16_rn(v);
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// (relaxed: the barriers' initialisation is published by its own fence and data by mbarriers; a release would
+// wait for every store of the thread, about 1 us here)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // CN (8, 16 or 32) consecutive fp32 columns of this thread's TMEM lane, and the wait for them
 template <int CN>
@@ -187,22 +189,22 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
   // The weights' first stages come to L2 while the preceding kernel finishes (a prefetch reads nothing
   // that could be stale); every read follows the wait.
   if (warp == 0 && lane < min(nb, C::NST)) tma_prefetch_l2_2d(&tm_w, (b0 + lane) * 128, n0);
-  if (warp == 2 && lane == 0) {
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], 1);
+  if (warp == 2) {  // a lane a barrier
+    if (lane < C::NST) {
+      mbar_init(&bars->full[lane], 1);
+      mbar_init(&bars->empty[lane], 1);
     }
-    for (int d = 0; d < C::ND; ++d) {
-      mbar_init(&bars->dfull[d], 1);
-      mbar_init(&bars->dempty[d], C::PW);
+    if (lane < C::ND) {
+      mbar_init(&bars->dfull[lane], 1);
+      mbar_init(&bars->dempty[lane], C::PW);
     }
-    for (int d = 0; d < 2; ++d) {
-      mbar_init(&bars->sfull[d], 1);
-      mbar_init(&bars->sempty[d], C::PW);
+    if (lane < 2) {
+      mbar_init(&bars->sfull[lane], 1);
+      mbar_init(&bars->sempty[lane], C::PW);
     }
-    mbar_init(&bars->received, 1);
+    if (lane == 0) mbar_init(&bars->received, 1);
     fence_mbar_init();
-    if (S > 1) mbar_arrive_expect_tx(&bars->received, (uint32_t)(S * rows * C::RLD * 4));
+    if (S > 1 && lane == 0) mbar_arrive_expect_tx(&bars->received, (uint32_t)(S * rows * C::RLD * 4));
   }
   if (warp == 1) {
     tmem_alloc(&bars->tmem_base, C::TCOLS);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
       const int k = lane % C::XC, b = min(b0 + c * C::XC + k, p.blocks - 1);
       const float w = ws[b];
       float* dst = scales + ((c & 1) * C::XC + k) * C::SLD;
-#pragma unroll
+#pragma unroll 1
       for (int r0 = 0; r0 < BN; r0 += 32) {
         float x[C::XC];
 #pragma unroll
@@ -380,27 +382,17 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
     __syncthreads();
     recv = part;
   }
-  // ---- sums of this CTA's rows: a lane takes a row and four tokens
-  for (int g = warp; ok && g < (rows + 31) / 32 * (BN / 4); g += C::THREADS / 32) {
-    const int c = g % (BN / 4) * 4, m = g / (BN / 4) * 32 + lane;
-    if (m >= rows) continue;
-    float4 v = *reinterpret_cast<const float4*>(recv + m * C::RLD + c);
-    for (int r = 1; r < S; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(recv + (r * share + m) * C::RLD + c);
-      v.x += x.x;
-      v.y += x.y;
-      v.z += x.z;
-      v.w += x.w;
-    }
-    const int n = n0 + lo + m;
-    const long t = t0 + c;
-    if (n < p.N) {
-      if (t < p.T) store_out(p, t, n, v.x);
-      if (t + 1 < p.T) store_out(p, t + 1, n, v.y);
-      if (t + 2 < p.T) store_out(p, t + 2, n, v.z);
-      if (t + 3 < p.T) store_out(p, t + 3, n, v.w);
-    }
-  }
+  // ---- sums of this CTA's rows: a lane takes a row, a warp a token at a time
+  if (ok)
+#pragma unroll 1
+    for (int c = warp; c < BN && t0 + c < p.T; c += C::THREADS / 32)
+#pragma unroll 1
+      for (int m = lane; m < rows && n0 + lo + m < p.N; m += 32) {
+        float v = 0.f;
+#pragma unroll 2
+        for (int r = 0; r < S; ++r) v += recv[(r * share + m) * C::RLD + c];
+        store_out(p, t0 + c, n0 + lo + m, v);
+      }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -485,18 +477,18 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   const int tiles = p.tiles_t * p.tiles_n;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], 1);
+  if (warp == 2) {  // a lane a barrier
+    if (lane < C::NST) {
+      mbar_init(&bars->full[lane], 1);
+      mbar_init(&bars->empty[lane], 1);
     }
-    for (int d = 0; d < C::ND; ++d) {
-      mbar_init(&bars->dfull[d], 1);
-      mbar_init(&bars->dempty[d], 16);  // the promoting warps of both CTAs
+    if (lane < C::ND) {
+      mbar_init(&bars->dfull[lane], 1);
+      mbar_init(&bars->dempty[lane], 16);  // the promoting warps of both CTAs
     }
-    for (int d = 0; d < 2; ++d) {
-      mbar_init(&bars->sfull[d], 2);
-      mbar_init(&bars->sempty[d], 8);
+    if (lane < 2) {
+      mbar_init(&bars->sfull[lane], 2);
+      mbar_init(&bars->sempty[lane], 8);
     }
     fence_mbar_init();
   }
@@ -506,7 +498,8 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers are ready before either signals the other's
+  cluster_arrive();
+  cluster_wait();  // both CTAs' barriers are ready before either signals the other's
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
