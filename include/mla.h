@@ -248,8 +248,9 @@ MLA_API mla_status mla_decode_attention_noalloc(const mla_dims* dims, const void
  *   - *_ld is the distance between consecutive rows in elements (bytes for codes), at least the
  *     row's width; elements between the width and *_ld are neither read nor written.
  *   - act_dtype is the element type of the unquantised rows: MLA_F32 or MLA_BF16.
- *   - Any width, alignment and *_ld is taken.  16-byte aligned rows (8-byte codes) whose width is
- *     a multiple of 8 take the faster, vectorised kernels.
+ *   - Any width and *_ld is taken, and any alignment of the elements' own size (less is
+ *     MLA_ERR_INVALID_ARG).  16-byte aligned rows (8-byte codes) whose width is a multiple of 8
+ *     take the faster, vectorised kernels.
  *   - They are launched with programmatic stream serialization like the projections above, but
  *     read and write nothing (L2 prefetches apart) before the preceding kernel has completed, so
  *     any of their inputs may be the output of the preceding call.

@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include <cstdlib>
+#include <initializer_list>
 
 #include "mla_internal.cuh"
 #include "decode_tc.cuh"
@@ -110,6 +111,17 @@ static mla_status check_act(int32_t act) {
   if (!dtype_ok(act)) return MLA_ERR_INVALID_ARG;
   return act == MLA_FP8_E4M3 ? MLA_ERR_UNSUPPORTED : MLA_OK;
 }
+
+// Whether pointers (null ones aside) are aligned to their element size.
+static bool aligned_to(size_t size, std::initializer_list<const void*> ptrs) {
+  uintptr_t bits = 0;
+  for (const void* p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
+  return (bits & (size - 1)) == 0;
+}
+static size_t act_size(int32_t act) { return act == MLA_F32 ? 4 : 2; }
+// Widths and counts beyond which the row operators' and the 8-bit projection's 32-bit indices would not
+// do (the tiles past the last row or value are counted in them too).
+constexpr int32_t kMaxExtent = 0x7fffffff - 4096;
 
 // The two partitioned kernels: the small-head one (at most 16 heads, bf16) and the tcgen05 one.
 // Both always run the length-balanced partition, whatever n_split says.
@@ -302,6 +314,9 @@ mla_status mla_norm_rows(int32_t act_dtype, const void* x, int64_t x_ld, const v
   if (x_ld < width || (residual && residual_ld < width) || (sum_out && sum_ld < width) ||
       (y && y_ld < width) || (codes && codes_ld < width))
     return MLA_ERR_INVALID_ARG;
+  if (!aligned_to(act_size(act_dtype), {x, residual, gamma, sum_out, y}) || !aligned_to(4, {scales}))
+    return MLA_ERR_INVALID_ARG;
+  if (n_tok > kMaxExtent || width > kMaxExtent) return MLA_ERR_UNSUPPORTED;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, residual, residual_ld, gamma, n_tok, width, eps,
@@ -317,6 +332,8 @@ mla_status mla_quantize_rows(int32_t act_dtype, const void* x, int64_t x_ld, int
   if (n_tok < 0 || width <= 0) return MLA_ERR_INVALID_ARG;
   if (n_tok == 0) return MLA_OK;
   if (!x || !codes || !scales || x_ld < width || codes_ld < width) return MLA_ERR_INVALID_ARG;
+  if (!aligned_to(act_size(act_dtype), {x}) || !aligned_to(4, {scales})) return MLA_ERR_INVALID_ARG;
+  if (n_tok > kMaxExtent || width > kMaxExtent) return MLA_ERR_UNSUPPORTED;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, nullptr, 0, nullptr, n_tok, width, 0.f,
@@ -334,6 +351,9 @@ mla_status mla_project_fp8(int32_t act_dtype, const uint8_t* x_codes, int64_t x_
   if (n_tok == 0) return MLA_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !out || x_ld < width || out_ld < n_out)
     return MLA_ERR_INVALID_ARG;
+  if (!aligned_to(act_size(act_dtype), {out}) || !aligned_to(4, {x_scales, w_scales}))
+    return MLA_ERR_INVALID_ARG;
+  if (n_tok > kMaxExtent || n_out > kMaxExtent || width > kMaxExtent) return MLA_ERR_UNSUPPORTED;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
   const Fp8Args a = {act_dtype, x_codes, x_ld, x_scales, w_codes, w_scales, n_tok, n_out, width,
@@ -352,6 +372,11 @@ mla_status mla_append_rows(const mla_dims* dims, const void* kv, int64_t kv_ld, 
   if ((s = check_cache(dims, cache)) != MLA_OK) return s;
   if (!kv || !seq_idx || !pos || !rope_cos || !rope_sin || rope_rows <= 0) return MLA_ERR_INVALID_ARG;
   if (kv_ld < (int64_t)dims->d_c + dims->d_rope) return MLA_ERR_INVALID_ARG;
+  const bool fp8 = dims->cache_dtype == MLA_FP8_E4M3;
+  if (!aligned_to(act_size(dims->act_dtype), {kv, gamma, fp8 ? nullptr : cache->rows, cache->rope}) ||
+      !aligned_to(4, {seq_idx, pos, rope_cos, rope_sin, cache->scales, cache->block_table}))
+    return MLA_ERR_INVALID_ARG;
+  if (n_tok > kMaxExtent || dims->d_c > kMaxExtent || dims->d_rope > kMaxExtent) return MLA_ERR_UNSUPPORTED;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
   return cuda_status(launch_append_rows(*dims, kv, kv_ld, n_tok, seq_idx, pos, gamma, eps, rope_cos,

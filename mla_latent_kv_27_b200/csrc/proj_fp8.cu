@@ -902,10 +902,13 @@ static cudaError_t launch_fp8_any(const Fp8Args& a, cudaStream_t st) {
 }
 
 // Output tiles go out by TMA stores (boxes of 16 outputs x 32 rows) where its alignment rules allow.
+static bool out_aligned(const Fp8Args& a) {
+  return (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_ld * (a.act == MLA_F32 ? 4 : 2) % 16 == 0;
+}
 static bool map_out(CUtensorMap* m, const Fp8Args& a) {
   auto enc = tmap_encoder();
   const int elt = a.act == MLA_F32 ? 4 : 2;
-  if (!enc || (reinterpret_cast<uintptr_t>(a.out) & 15) || (a.out_ld * elt) % 16) return false;
+  if (!enc || !out_aligned(a)) return false;
   cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.T};
   cuuint64_t strides[1] = {(cuuint64_t)(a.out_ld * elt)};
   cuuint32_t box[2] = {16, 32};
@@ -972,6 +975,8 @@ static bool tma_layout(const Fp8Args& a) {
 //   few tokens, 128 columns   waves (0.40 blocks per CTA + 7) + 1.5     128x7168x16384: 36 (64 columns: 50)
 //   many tokens, 128 outputs  waves (0.26 blocks + 0.75) + 4            256x7168x16384: 40 (few-token: 60)
 //   many tokens, 160 outputs  waves (0.307 blocks + 1.3) + 4            2048x7168x16384: 240 (128 outputs: 290)
+// and 3.5 more a wave of the many-token kernel whose output rows TMA stores do not take
+// (333x1999x2000: 12.6, few-token 10.4).
 template <int BN>
 static float skinny_us(const Fp8Args& a, float block, float wave) {
   const int blocks = (a.K + 127) / 128, S = skinny_split<BN>(a);
@@ -981,7 +986,7 @@ static float skinny_us(const Fp8Args& a, float block, float wave) {
 }
 static float wide_us(const Fp8Args& a, int wn, float block, float wave) {
   const long tiles = (long)((a.N + wn - 1) / wn) * ((a.T + 255) / 256);
-  return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave) + 4.f;
+  return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave + (out_aligned(a) ? 0.f : 3.5f)) + 4.f;
 }
 
 cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {

@@ -184,3 +184,44 @@ def test_captured_and_replayed_with_new_inputs(lib):
         graph.replay()
         torch.cuda.synchronize()
         check(o, *reference(x, xs, w, ws, t, n, k), k)
+
+
+def test_offsets_past_32_bits(lib):
+    """300 001 rows of 7168 values and 8000 outputs: the last ones lie past 2^31 bytes of x and 2^32
+    bytes of out.  The first and last rows are compared."""
+    t, n, k = 300_001, 8000, 7168
+    x = torch.zeros((t, k), dtype=torch.uint8, device="cuda")
+    x[:300], x[-300:] = codes((300, k), 1), codes((300, k), 2)
+    xs = torch.ones((t, 56), device="cuda")
+    xs[:300], xs[-300:] = scales((300, 56), 3), scales((300, 56), 4)
+    w, ws = codes((n, k), 5), scales((63, 56), 6)
+    out = torch.full((t, n), GUARD, dtype=torch.bfloat16, device="cuda")
+    lib.mla_project_fp8(lib.MLA_BF16, x, k, xs, t, w, ws, n, k, out, n)
+    torch.cuda.synchronize()
+    assert lib.mla_check_device_error()[0] == 0
+    for part in (slice(0, 300), slice(t - 300, t)):
+        check(out[part], *reference(x[part], xs[part], w, ws, 300, n, k), k)
+    assert not out[300:-300].any()
+
+
+def test_chain_of_calls_without_a_wait_between(lib):
+    """Each call's output is the next one's input, many times over, on one stream with nothing between:
+    equal, bit for bit, to the same calls with a synchronisation after each."""
+    t, k = 40, 1024
+    w, ws = codes((k, k), 2), scales((8, 8), 3) / 2 ** 7
+    g = torch.ones(k, device="cuda")
+
+    def run_chain(wait):
+        x = torch.randn((t, k), generator=gen(1), device="cuda")
+        q, s = torch.empty((t, k), dtype=torch.uint8, device="cuda"), torch.empty((t, 8), device="cuda")
+        r = x.clone()
+        for _ in range(30):
+            lib.mla_norm_rows(lib.MLA_F32, x, k, r, k, g, t, k, 1e-6, r, k, None, 0, q, k, s)
+            wait()
+            lib.mla_project_fp8(lib.MLA_F32, q, k, s, t, w, ws, k, k, x, k)
+            wait()
+        torch.cuda.synchronize()
+        return r, x
+
+    a, b = run_chain(lambda: None), run_chain(torch.cuda.synchronize)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.isfinite(a[1]).all()

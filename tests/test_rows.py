@@ -388,3 +388,76 @@ def test_rows_captured_and_replayed_with_new_inputs(lib):
         torch.cuda.synchronize()
         near(y, norm_ref(x, res, g, 1e-6)[1])
         check_codes(q, s, y.double(), width, 2.0 ** -24)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_norm_and_quantize_offsets_past_32_bits(lib):
+    """300 001 rows of 7168: the last ones lie past 2^31 elements (bf16) and bytes (codes)."""
+    t, width = 300_001, 7168
+    x = torch.empty((t, width), dtype=torch.bfloat16, device="cuda")
+    x[:8], x[-8:] = randn((8, width), 1).bfloat16(), randn((8, width), 2).bfloat16()
+    x[8:-8] = 1
+    q = torch.empty((t, width), dtype=torch.uint8, device="cuda")
+    s = torch.empty((t, 56), device="cuda")
+    for norm in (True, False):
+        q.fill_(99)
+        if norm:
+            lib.mla_norm_rows(lib.MLA_BF16, x, width, None, 0, None, t, width, 1e-6, None, 0, None, 0, q, width, s)
+        else:
+            lib.mla_quantize_rows(lib.MLA_BF16, x, width, t, width, q, width, s)
+        torch.cuda.synchronize()
+        for part in (slice(0, 8), slice(t - 8, t)):
+            y = norm_ref(x[part], None, None, 1e-6)[1] if norm else x[part].double()
+            check_codes(q[part], s[part], y, width, REL if norm else 2.0 ** -24)
+    assert lib.mla_check_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("act,kind", KINDS)
+def test_append_rows_offsets_past_32_bits(lib, act, kind):
+    """Pages whose rows lie past 2^31 elements of the pool (2^32 bytes for the 8-bit one)."""
+    d_c, d_rope, pages = 512, 64, 60_000 if kind != "fp8" else 140_000
+    c = Cache(lib, act, kind, d_c, d_rope, 64, (128,))
+    for name in ("rows", "scales", "rope"):
+        old = getattr(c, name)
+        if old is not None:
+            setattr(c, name, torch.zeros((pages * 64, old.shape[1]), dtype=old.dtype, device="cuda"))
+    c.table = torch.tensor([[pages - 1, 0]], dtype=torch.int32, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    c.desc = lib.mla_cache(p(c.rows), p(c.scales), p(c.rope), c.table.data_ptr(), 2, pages, 1)
+    kv = randn((128, 576), 5).to(act)
+    seq = torch.zeros(128, dtype=torch.int32, device="cuda")
+    pos = torch.arange(128, dtype=torch.int32, device="cuda")
+    cos, sin = rope_tables(lib, d_rope, 128)
+    lib.mla_append_rows(c.dims, kv, 576, 128, seq, pos, None, 0.0, cos, sin, 128, c.desc)
+    torch.cuda.synchronize()
+    assert lib.mla_check_device_error()[0] == 0
+    at = c.slots(seq, pos)
+    if kind == "fp8":
+        check_codes(c.rows[at], c.scales[at], kv[:, :512].double(), 512, 2.0 ** -24)
+    else:
+        near(c.rows[at][:, :512], kv[:, :512].double(), 0.0)
+    assert not c.rows[64:(pages - 1) * 64].any()
+
+
+def test_calls_follow_the_current_stream(lib):
+    """Without a stream argument a call goes to torch's current stream."""
+    t, width = 2000, 4096
+    st = torch.cuda.Stream()
+    x = torch.zeros((t, width), dtype=torch.bfloat16, device="cuda")
+    q, s = torch.empty((t, width), dtype=torch.uint8, device="cuda"), torch.empty((t, 32), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):
+            x.add_(0.25)  # (in order only on the same stream)
+        lib.mla_quantize_rows(lib.MLA_BF16, x, width, t, width, q, width, s)
+    st.synchronize()
+    check_codes(q, s, torch.full((t, width), 5.0, dtype=torch.float64, device="cuda"), width, 2.0 ** -24)
+
+
+def test_tensors_on_no_or_another_device_are_refused(lib):
+    x = torch.zeros((2, 64), device="cuda")
+    host = torch.zeros((2, 64))
+    with pytest.raises(ValueError):
+        lib.mla_quantize_rows(lib.MLA_F32, host, 64, 2, 64, x, 64, x)
+    with pytest.raises(lib.MlaError):
+        lib.mla_quantize_rows(lib.MLA_F32, x, 63, 2, 64, x, 64, x)

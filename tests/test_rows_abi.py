@@ -92,3 +92,37 @@ def test_host_tensors_are_refused(mla):
     x = torch.zeros((2, 64))
     with pytest.raises(ValueError):
         mla.mla_quantize_rows(mla.MLA_F32, x, 64, 2, 64, 4096, 64, 4096, stream=0)
+
+
+def test_addresses_between_elements_are_refused(mla):
+    """A pointer that is no multiple of its element's size would fault on the device."""
+    for name in ("x", "res", "gamma", "so", "y"):
+        assert norm(mla, **{name: P + 1}) == INVALID
+        assert norm(mla, act=mla.MLA_F32, **{name: P + 2}) == INVALID
+    assert norm(mla, scales=P + 2) == INVALID
+    lib = mla.lib_handle()
+    assert lib.mla_quantize_rows(mla.MLA_BF16, P + 1, 64, 2, 64, P, 64, P, None) == INVALID
+    assert lib.mla_quantize_rows(mla.MLA_BF16, P, 64, 2, 64, P, 64, P + 1, None) == INVALID
+    for k in (3, 6, 9):
+        a = [mla.MLA_F32, P, 64, P, 2, P, P, 8, 64, P, 8, None]
+        a[k] = P + 2
+        assert lib.mla_project_fp8(*a) == INVALID
+    d = mla.mla_dims(64, 64, 16, 32, 32, 4, 64, mla.MLA_F32, mla.MLA_F32, 0.1)
+    for k in (1, 4, 5, 6, 8, 9):
+        c = mla.mla_cache(P, None, None, P, 4, 8, 2)
+        a = [ctypes.byref(d), P, 80, 2, P, P, P, 0.0, P, P, 16, ctypes.byref(c), None]
+        a[k] = P + 2
+        assert lib.mla_append_rows(*a) == INVALID
+    c = mla.mla_cache(P + 2, None, None, P, 4, 8, 2)
+    assert lib.mla_append_rows(ctypes.byref(d), P, 80, 2, P, P, P, 0.0, P, P, 16, ctypes.byref(c), None) == INVALID
+
+
+def test_extents_past_the_index_range_are_refused(mla):
+    big = 2 ** 31 - 1
+    assert norm(mla, n=big) == UNSUPPORTED
+    assert norm(mla, width=big, x_ld=big, res_ld=big, so_ld=big, y_ld=big, codes_ld=big) == UNSUPPORTED
+    lib = mla.lib_handle()
+    assert lib.mla_quantize_rows(mla.MLA_BF16, P, 64, big, 64, P, 64, P, None) == UNSUPPORTED
+    assert lib.mla_project_fp8(mla.MLA_F32, P, 64, P, big, P, P, 8, 64, P, 8, None) == UNSUPPORTED
+    assert lib.mla_project_fp8(mla.MLA_F32, P, big, P, 2, P, P, 8, big, P, 8, None) == UNSUPPORTED
+    assert lib.mla_project_fp8(mla.MLA_F32, P, 64, P, 2, P, P, big, 64, P, big, None) == UNSUPPORTED
