@@ -37,7 +37,10 @@
  *     (w_dkv, w_kr, w_uk, w_uv), and q_nope in mla_absorb_query; everything else
  *     they read, and everything they write, comes after the wait.  So a weight (or query
  *     input) must not be an output of the immediately preceding library call on the same
- *     stream.  Setting MLA_PDL=0 in the environment (read once) launches them normally.
+ *     stream.  (Calls before that one have completed: a kernel lets the next one start only
+ *     after its own wait.)  One exception: q_nope may come from mla_project_fp8 directly in front,
+ *     called by the same host thread; mla_absorb_query is then launched normally.
+ *     Setting MLA_PDL=0 in the environment (read once) launches them all normally.
  */
 #ifndef MLA_H_
 #define MLA_H_

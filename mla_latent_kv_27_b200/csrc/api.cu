@@ -84,6 +84,20 @@ bool pdl_enabled() {
   return on;
 }
 
+// The calling thread's latest call that enqueued work: its stream, and whether it was the 8-bit
+// projection.  The absorb kernel reads q_nope before it waits for the kernel in front of it, so it is
+// launched without programmatic overlap unless that kernel is known to be another call of this
+// library: the projection may have written q_nope.  (Only the kernel directly in front matters:
+// every kernel lets the next one start after its own wait, when all before it have completed.)
+static thread_local const void* t_stream = nullptr;
+static thread_local bool t_known = false, t_projected = false;
+static void note_call(const void* stream, bool projected = false) {
+  t_stream = stream;
+  t_known = true;
+  t_projected = projected;
+}
+static bool absorb_may_overlap(const void* stream) { return t_known && t_stream == stream && !t_projected; }
+
 static mla_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
   if (e == kUnsupported) return MLA_ERR_UNSUPPORTED;
@@ -199,6 +213,7 @@ mla_status mla_append_cache(const mla_dims* dims, const void* h, int32_t n_tok,
   if (workspace_bytes < need || (need > 0 && !workspace)) return MLA_ERR_INVALID_ARG;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
+  note_call(stream);
   return cuda_status(launch_append(*dims, h, n_tok, seq_idx, pos, w_dkv, w_kr, rope_cos, rope_sin,
                                    rope_rows, make_view(dims, cache), static_cast<float*>(workspace),
                                    err, static_cast<cudaStream_t>(stream)));
@@ -216,8 +231,10 @@ mla_status mla_absorb_query(const mla_dims* dims, const void* q_nope, const void
     return MLA_ERR_INVALID_ARG;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
+  const bool overlap = absorb_may_overlap(stream);
+  note_call(stream);
   return cuda_status(launch_absorb(*dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin,
-                                   rope_rows, q_packed, err, static_cast<cudaStream_t>(stream)));
+                                   rope_rows, q_packed, err, overlap, static_cast<cudaStream_t>(stream)));
 }
 
 size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t s_q,
@@ -278,6 +295,7 @@ mla_status mla_decode_attention(const mla_dims* dims, const void* q_packed,
   a.o_lat = o_lat;
   a.lse = lse;
   a.err = err;
+  note_call(stream);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // the partitioned launchers run their own combine
   const DecodePath path = decode_path(dims);
@@ -298,6 +316,7 @@ mla_status mla_output_up(const mla_dims* dims, const void* o_lat, int32_t n_tok,
   if (!o_lat || !w_uv || !out) return MLA_ERR_INVALID_ARG;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
+  note_call(stream);
   return cuda_status(launch_output_up(*dims, o_lat, n_tok, w_uv, out, err, static_cast<cudaStream_t>(stream)));
 }
 
@@ -321,6 +340,7 @@ mla_status mla_norm_rows(int32_t act_dtype, const void* x, int64_t x_ld, const v
   if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, residual, residual_ld, gamma, n_tok, width, eps,
                       sum_out, sum_ld, y, y_ld, codes, codes_ld, scales, err};
+  note_call(stream);
   return cuda_status(launch_rows(a, true, static_cast<cudaStream_t>(stream)));
 }
 
@@ -338,6 +358,7 @@ mla_status mla_quantize_rows(int32_t act_dtype, const void* x, int64_t x_ld, int
   if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, nullptr, 0, nullptr, n_tok, width, 0.f,
                       nullptr, 0, nullptr, 0, codes, codes_ld, scales, err};
+  note_call(stream);
   return cuda_status(launch_rows(a, false, static_cast<cudaStream_t>(stream)));
 }
 
@@ -358,6 +379,7 @@ mla_status mla_project_fp8(int32_t act_dtype, const uint8_t* x_codes, int64_t x_
   if (!err) return MLA_ERR_CUDA;
   const Fp8Args a = {act_dtype, x_codes, x_ld, x_scales, w_codes, w_scales, n_tok, n_out, width,
                      out, out_ld, err};
+  note_call(stream, true);
   return cuda_status(launch_project_fp8(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -379,6 +401,7 @@ mla_status mla_append_rows(const mla_dims* dims, const void* kv, int64_t kv_ld, 
   if (n_tok > kMaxExtent || dims->d_c > kMaxExtent || dims->d_rope > kMaxExtent) return MLA_ERR_UNSUPPORTED;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
+  note_call(stream);
   return cuda_status(launch_append_rows(*dims, kv, kv_ld, n_tok, seq_idx, pos, gamma, eps, rope_cos,
                                         rope_sin, rope_rows, make_view(dims, cache), err,
                                         static_cast<cudaStream_t>(stream)));

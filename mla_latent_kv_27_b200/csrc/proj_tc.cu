@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = bars->tmem_base;
   bool ok = true;
 
-  griddep_launch_dependents();
   if (nk > 0) {
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------ TMA producer
@@ -146,6 +145,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int first = min(nk, NST);
       for (int i = 0; i < first; ++i) load_a(i);
       griddep_wait();
+      // only now may the next grid start: what it reads before its own wait (weights, q_nope) can then
+      // not be under way in a grid before this one
+      griddep_launch_dependents();
       for (int i = 0; i < first; ++i) load_b(i);
       for (int i = first; i < nk; ++i) {
         const int s = i % NST;
@@ -351,7 +353,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (S > 1) cluster_arrive();  // peers may write into this CTA's receive buffer after this
-  griddep_launch_dependents();
   const uint32_t tmem = bars->tmem_base;
   bool ok = true;
 
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   } else {
     // the cache may still be read by an earlier grid of the stream until it completes
     griddep_wait();
+    if (threadIdx.x == 64) griddep_launch_dependents();  // (after the wait, as in wgemm_kernel)
     // page slots of the tokens this CTA finishes (errors reported by the first m-tile only)
     const int e = threadIdx.x - 64;
     for (int i = e; i < own; i += 128) {
@@ -880,7 +882,7 @@ bool tc_absorb_fused_supported(const mla_dims& d) {
 
 cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* q_rope, const int32_t* q_pos,
                              int n_tok, const void* w_uk, const float* rcos, const float* rsin, int rope_rows,
-                             void* q_packed, int* err, cudaStream_t st) {
+                             void* q_packed, int* err, bool overlap, cudaStream_t st) {
   if (n_tok <= 0) return cudaSuccess;
   if ((n_tok + 63) / 64 > 65535) return kUnsupported;
   // 16-byte vector loads and stores of the RoPE part (callers check with absorb_tc_aligned)
@@ -920,7 +922,7 @@ cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  cfg.numAttrs = pdl_enabled() && overlap ? 1 : 0;  // (q_nope is read before the wait)
   e = cudaLaunchKernelEx(&cfg, ptc::absorb_tc_kernel, mw, mq, mo, p);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

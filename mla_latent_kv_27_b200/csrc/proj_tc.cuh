@@ -11,7 +11,7 @@ bool tc_absorb_fused_supported(const mla_dims& d);
 bool absorb_tc_aligned(const void* q_rope, const void* q_packed, const float* rcos, const float* rsin);
 cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* q_rope, const int32_t* q_pos,
                              int n_tok, const void* w_uk, const float* rcos, const float* rsin, int rope_rows,
-                             void* q_packed, int* err, cudaStream_t st);
+                             void* q_packed, int* err, bool overlap, cudaStream_t st);
 // q_packed[t, h, 0:d_c] = W_UK[h]^T q_nope[t, h]  (bf16)
 cudaError_t launch_absorb_gemm_tc(const mla_dims& d, const void* q_nope, int n_tok, const void* w_uk,
                                   void* q_packed, int* err, cudaStream_t st);

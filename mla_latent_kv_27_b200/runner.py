@@ -316,9 +316,9 @@ class MLALayer(MLARunner):
 
         mla_norm_rows        r = x + residual, its norm as 8-bit rows
         mla_project_fp8      [q_rank | d_c | d_rope] = W_down r
-        mla_append_rows      the latent normed, the rotary key rotated -> cache
         mla_norm_rows        the query latent's norm as 8-bit rows
         mla_project_fp8 x 2  q_nope and q_rope of all heads
+        mla_append_rows      the latent normed, the rotary key rotated -> cache
         mla_absorb_query, mla_decode_attention, mla_output_up
         mla_quantize_rows    the heads' outputs as 8-bit rows
         mla_project_fp8      y = W_O out
@@ -363,15 +363,15 @@ class MLALayer(MLARunner):
                         None, 0, self.x8, D, self.x8_s, st)
         B.mla_project_fp8(self.act, self.x8, D, self.x8_s, T, self.w_down, self.s_down, self.d_down, D, self.down,
                           self.d_down, st)
-        B.mla_append_rows(self.dims, self.down[:, R:], self.d_down, T, self.seq_idx, self.pos, self.g_kv, self.eps,
-                          self.rope_cos, self.rope_sin, self.rope_rows, self.cache.desc, st)
         B.mla_norm_rows(self.act, self.down, self.d_down, None, 0, self.g_q, T, R, self.eps, None, 0, None, 0,
                         self.q8, R, self.q8_s, st)
-        # q_nope first: the absorb reads it before the call in front of it (q_rope's) has completed
         B.mla_project_fp8(self.act, self.q8, R, self.q8_s, T, self.w_qn, self.s_qn, w.n_heads * w.d_nope, R,
                           self.q_nope, w.n_heads * w.d_nope, st)
         B.mla_project_fp8(self.act, self.q8, R, self.q8_s, T, self.w_qr, self.s_qr, w.n_heads * w.d_rope, R,
                           self.q_rope, w.n_heads * w.d_rope, st)
+        # (here, so that the absorb, which reads q_nope early, may start under it)
+        B.mla_append_rows(self.dims, self.down[:, R:], self.d_down, T, self.seq_idx, self.pos, self.g_kv, self.eps,
+                          self.rope_cos, self.rope_sin, self.rope_rows, self.cache.desc, st)
         self.absorb(st)
         self.decode(st)
         self.output(st)

@@ -125,3 +125,37 @@ def test_layer_step_captured(lib):
         torch.cuda.synchronize()
         assert torch.equal(got, L.y)
     assert lib.mla_check_device_error()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("between", [False, True])
+def test_absorb_directly_behind_the_projection(lib, between):
+    """q_nope written by mla_project_fp8 directly in front of the absorb (or one append before it), which
+    reads q_nope early: equal, bit for bit, to the same calls with a synchronisation between."""
+    from mla_latent_kv_27_b200.runner import MLALayer
+    w = dataclasses.replace(W["v3_bf16"], d_model=512)
+    L = MLALayer(w, 1536, lengths=(130,) * 40)
+    L.draw_step_inputs()
+    T, n = L.n_tok, w.n_heads * w.d_nope
+
+    def project_and_absorb(wait):
+        lib.mla_quantize_rows(L.act, x, 1536, T, 1536, L.q8, 1536, L.q8_s)
+        wait()
+        lib.mla_project_fp8(L.act, L.q8, 1536, L.q8_s, T, L.w_qn, L.s_qn, n, 1536, L.q_nope, n)
+        wait()
+        if between:
+            L.append()
+            wait()
+        L.absorb()
+
+    for seed in range(6):
+        x = torch.randn((T, 1536), generator=torch.Generator(device="cuda").manual_seed(seed),
+                        device="cuda").bfloat16()
+        torch.cuda.synchronize()
+        project_and_absorb(lambda: None)
+        torch.cuda.synchronize()
+        got = L.q_packed.clone()
+        L.q_packed.zero_()
+        project_and_absorb(torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        assert torch.equal(got, L.q_packed)
