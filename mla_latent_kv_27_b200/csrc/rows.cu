@@ -378,9 +378,9 @@ __global__ void __launch_bounds__(RW_WARPS * 32) rows_warp_kernel(const RowsArgs
 // at its launch).  A stage holds a row of x and, after it, the residual's; it is refilled once
 // every thread has its values in registers, which the barrier of the row's sum shows.
 constexpr int RS_MAX_STAGES = 8;
-constexpr int RS_SMEM = 110 * 1024;
-constexpr int RS_ROWS = 600;
-constexpr int LOOP_THREADS = 1024;
+constexpr int RS_SMEM = 220 * 1024;  // of an SM, for its streaming CTAs
+constexpr int RS_ROWS = 300;         // per CTA of an SM: about two rows each
+constexpr int LOOP_THREADS = 1024;   // threads of an SM's walking CTAs (1536 and 2048: 8 and 2 % slower)
 
 template <typename T, int CH, int NT>
 __global__ void __launch_bounds__(NT) rows_stream_kernel(const RowsArgs a, int stages, int gamma_staged) {
@@ -805,21 +805,33 @@ static cudaError_t rows_impl(const RowsArgs& a, bool norm, cudaStream_t st) {
     if (ctas * RQ_WARPS > 0x7fffffffl) return kUnsupported;
     return launch_pdl(rows_quantize_kernel<T>, (unsigned)ctas, RQ_WARPS * 32, st, 0, a, units);
   }
+  // Which kernel (us on B200, bf16; its neighbour's time in brackets):
+  //   up to 512 values    a warp per row          16384 x 512: 11 [a CTA per row 18]
+  //   up to 2048          a CTA per row, then     391 x 1536: 2.2 [walking CTAs 2.9]
+  //                       walking CTAs            16384 x 1536 with the residual: 38 [43]
+  //   up to 16384         a CTA per row, then     500 x 7168: 8.7 [streaming 9.9]
+  //                       streaming CTAs          8191 x 7168: 87 [a CTA per row 129]; 3583 x 16384: 95 [132]
+  //   up to 32768         a CTA per row
+  auto threads = [&](int ch) { return (unsigned)(((chunks + ch - 1) / ch + 31) / 32 * 32); };
   if (chunks <= 64)
     return launch_pdl(rows_warp_kernel<T, 2>, ((unsigned)a.n_tok + RW_WARPS - 1) / RW_WARPS, RW_WARPS * 32, st, 0, a);
-  // many rows: persistent CTAs, two per SM, rows streamed through shared memory
-  const int one = a.width * (int)sizeof(T), row_bytes = a.residual ? 2 * one : one, fixed = a.gamma && !(a.sum_out && a.y) ? one : 0;
-  const int stages = min(RS_MAX_STAGES, (RS_SMEM - fixed) / row_bytes);
-  if (a.n_tok >= RS_ROWS && stages >= 2 && chunks > 256 && chunks <= 1024) {
-    auto kernel = rows_stream_kernel<T, 2, 512>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RS_SMEM);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, min(a.n_tok, 2 * 148), ((chunks + 1) / 2 + 31) / 32 * 32, st, stages * row_bytes + fixed, a, stages, fixed > 0 ? 1 : 0);
+  if (chunks <= 256) {
+    const int at_once = 148 * (LOOP_THREADS / (int)threads(1));
+    if (a.n_tok <= at_once) return launch_pdl(rows_kernel<T, 1, 256>, (unsigned)a.n_tok, threads(1), st, 0, a);
+    return launch_pdl(rows_loop_kernel<T>, at_once, threads(1), st, 0, a);
   }
-  auto threads = [&](int ch) { return (unsigned)(((chunks + ch - 1) / ch + 31) / 32 * 32); };
-  if (chunks <= 256)
-    return launch_pdl(rows_loop_kernel<T>, min(a.n_tok, 148 * (LOOP_THREADS / (int)threads(1))), threads(1), st, 0, a);
-  if (chunks <= 1024) return launch_pdl(rows_kernel<T, 2, 512>, (unsigned)a.n_tok, threads(2), st, 0, a);
+  const int per_sm = chunks <= 1024 ? 2 : 1, room = RS_SMEM / per_sm;
+  const int one = a.width * (int)sizeof(T), row_bytes = a.residual ? 2 * one : one;
+  const int fixed = a.gamma && !(a.sum_out && a.y) ? one : 0;  // the weight's copy (see the kernel)
+  const int stages = min(RS_MAX_STAGES, (room - fixed) / row_bytes);
+  if (a.n_tok >= RS_ROWS * per_sm && chunks <= 2048 && stages >= 2) {
+    auto kernel = chunks <= 1024 ? rows_stream_kernel<T, 2, 512> : rows_stream_kernel<T, 2, 1024>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, min(a.n_tok, per_sm * 148), threads(2), st, stages * row_bytes + fixed, a, stages,
+                      fixed > 0 ? 1 : 0);
+  }
+  if (chunks <= 1024) return launch_pdl(rows_kernel<T, 1, 1024>, (unsigned)a.n_tok, threads(1), st, 0, a);
   return launch_pdl(rows_kernel<T, 4, 1024>, (unsigned)a.n_tok, threads(4), st, 0, a);
 }
 
