@@ -587,16 +587,18 @@ __device__ __forceinline__ void report(const AppendParams& p, const Place& r) {
 
 constexpr int AR_WARPS = 4;
 
-// One warp per token: lane l holds chunks l, l + 32, ... of 8 latent values (CH of them, 16 lanes a
-// 128-value block) and, below d_rope / 8 lanes, one chunk of the rotary key.  A warp walks tokens w,
-// w + (warps of the grid), ... with the next token's row and its page id (whose position came one
-// token earlier still) under way; a token a warp waited for each of these in turn.
-template <typename T, int CH, bool FP8>
+// LANES lanes (16 or 32) per token: lane l holds chunks l, l + LANES, ... of 8 latent values (CH of
+// them, 16 lanes a 128-value block) and one chunk of the rotary key below d_rope / 8 lanes.  A group of
+// lanes walks tokens w, w + (groups of the grid), ... with the next token's row and its page id (whose
+// position came one token earlier still) under way; a token a warp waited for each of these in turn.
+// With 16 lanes a warp's instructions serve two tokens, and these kernels issue for half of their time.
+template <typename T, int LANES, int CH, bool FP8>
 __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x % 32;
-  const long stride = (long)gridDim.x * AR_WARPS;
+  constexpr int PER_WARP = 32 / LANES;
+  const int lane = threadIdx.x % LANES;
+  const long stride = (long)gridDim.x * AR_WARPS * PER_WARP;
   const T* gamma = static_cast<const T*>(p.gamma);
   const int chunks = p.d_c / 8;
   const bool rot = lane < p.d_rope / 8;
@@ -605,53 +607,55 @@ __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const Append
   for (int i = 0; i < CH; ++i) {
     g[i] = {};
     nv[i] = {};
-    if (gamma && lane + 32 * i < chunks) g[i] = raw8(gamma + 8 * (lane + 32 * i));
+    if (gamma && lane + LANES * i < chunks) g[i] = raw8(gamma + 8 * (lane + LANES * i));
   }
-  long t = (long)blockIdx.x * AR_WARPS + threadIdx.x / 32;
-  auto fetch = [&](long t) {
-    const T* src = static_cast<const T*>(p.kv) + t * p.kv_ld;
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-      if (lane + 32 * i < chunks) nv[i] = raw8(src + 8 * (lane + 32 * i));
-    if (rot) nk = raw8(src + p.d_c + 8 * lane);
-  };
-  int seq = 0, ps = 0;    // of the token after the current one
+  // first token of the warp (the same in all lanes), and this group's
+  long t0 = ((long)blockIdx.x * AR_WARPS + threadIdx.x / 32) * PER_WARP;
+  const int sub = threadIdx.x % 32 / LANES;
+  int seq = 0, ps = 0;  // of the token after the current one
   auto where = [&](long t) {
+    if (t >= p.T) return;
     seq = p.seq_idx[t];
     ps = p.pos[t];
   };
-  if (t >= p.T) return;
-  where(t);
-  fetch(t);
-  Place here = place_of(p, seq, ps);
-  if (t + stride < p.T) where(t + stride);
-  for (; t < p.T; t += stride) {
+  Place here = {0, 0, PLACE_SEQ, 0};
+  auto fetch = [&](long t) {
+    if (t >= p.T) return;
+    const T* src = static_cast<const T*>(p.kv) + t * p.kv_ld;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (lane + LANES * i < chunks) nv[i] = raw8(src + 8 * (lane + LANES * i));
+    if (rot) nk = raw8(src + p.d_c + 8 * lane);
+    here = place_of(p, seq, ps);
+  };
+  where(t0 + sub);
+  fetch(t0 + sub);
+  where(t0 + sub + stride);
+  for (; t0 < p.T; t0 += stride) {
+    const long t = t0 + sub;
     Eight v[CH], k = load8(reinterpret_cast<const T*>(&nk));
 #pragma unroll
     for (int i = 0; i < CH; ++i) v[i] = load8(reinterpret_cast<const T*>(&nv[i]));
     const Place now = here;
-    const bool ok = now.pid >= 0 && now.pid < p.cv.num_pages;
+    const bool ok = t < p.T && now.pid >= 0 && now.pid < p.cv.num_pages;
     float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
     if (rot && ok) {
       const long at = (long)now.pos * (p.d_rope / 2) + 4 * lane;
       cs = *reinterpret_cast<const float4*>(p.rcos + at);
       sn = *reinterpret_cast<const float4*>(p.rsin + at);
     }
-    if (t + stride < p.T) {
-      fetch(t + stride);
-      here = place_of(p, seq, ps);
-      if (t + 2 * stride < p.T) where(t + 2 * stride);
-    }
-    if (!ok) {
-      if (lane == 0) report(p, now);
-      continue;
-    }
-    const long slot = (long)now.pid * p.cv.page_size + now.row;
+    fetch(t + stride);
+    where(t + 2 * stride);
+    if (t < p.T && !ok && lane == 0) report(p, now);
+    const long slot = (long)now.pid * p.cv.page_size + now.row;  // (used where ok)
     if (gamma) {
       uint64_t sq = 0ull;
 #pragma unroll
       for (int i = 0; i < CH; ++i) squares8(sq, v[i]);
-      const float inv = __frsqrt_rn(warp_sum(pair_sum(sq)) / (float)p.d_c + p.eps);
+      float ss = pair_sum(sq);
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = __frsqrt_rn(ss / (float)p.d_c + p.eps);
 #pragma unroll
       for (int i = 0; i < CH; ++i) v[i] = mul8(scale8(v[i], inv), load8(reinterpret_cast<const T*>(&g[i])));
     }
@@ -671,21 +675,21 @@ __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const Append
       block_scales<CH>(m, s, inv);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = lane + 32 * i;
-        if (c < chunks) {
+        const int c = lane + LANES * i;
+        if (ok && c < chunks) {
           *reinterpret_cast<uint2*>(q + 8 * c) = codes8(v[i], inv[i]);
           if (c % 16 == 0) sc[c / 16] = s[i];
         }
       }
-      if (rot) store8(static_cast<__nv_bfloat16*>(p.cv.rope) + slot * p.d_rope + 8 * lane, k);
+      if (ok && rot) store8(static_cast<__nv_bfloat16*>(p.cv.rope) + slot * p.d_rope + 8 * lane, k);
     } else {
       T* row = static_cast<T*>(p.cv.rows) + slot * (p.d_c + p.d_rope);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = lane + 32 * i;
-        if (c < chunks) store8(row + 8 * c, v[i]);
+        const int c = lane + LANES * i;
+        if (ok && c < chunks) store8(row + 8 * c, v[i]);
       }
-      if (rot) store8(row + p.d_c + 8 * lane, k);
+      if (ok && rot) store8(row + p.d_c + 8 * lane, k);
     }
   }
 }
@@ -848,11 +852,20 @@ static cudaError_t append_rows_impl(const rows::AppendParams& p, cudaStream_t st
                    aligned(p.kv, 16) && aligned(p.gamma, 16) && aligned(p.rcos, 16) && aligned(p.rsin, 16) &&
                    aligned(p.cv.rows, 16) && (!FP8 || aligned(p.cv.rope, 16));
   if (!vec) return launch_pdl(append_rows_any_kernel<T, FP8>, (unsigned)ctas, AR_WARPS * 32, st, 0, p);
-  const long at_once = 148 * (sizeof(T) == 4 ? 4 : 5);  // what the registers of d_c = 512 (116 and 96) let run at once
-  const unsigned grid = (unsigned)(ctas < at_once ? ctas : at_once);
-  if (p.d_c <= 256) return launch_pdl(append_rows_kernel<T, 1, FP8>, grid, AR_WARPS * 32, st, 0, p);
-  if (p.d_c <= 512) return launch_pdl(append_rows_kernel<T, 2, FP8>, grid, AR_WARPS * 32, st, 0, p);
-  return launch_pdl(append_rows_kernel<T, 4, FP8>, grid, AR_WARPS * 32, st, 0, p);
+  // as many CTAs as run at once
+  auto go = [&](auto kernel, int per_warp, int per_sm) {
+    const long warps = ((long)p.T + per_warp - 1) / per_warp, ctas = (warps + AR_WARPS - 1) / AR_WARPS;
+    return launch_pdl(kernel, (unsigned)(ctas < 148 * per_sm ? ctas : 148 * per_sm), AR_WARPS * 32, st, 0, p);
+  };
+  if (p.d_c <= 512 && p.d_rope <= 128) {
+    // a token a warp while that is shorter: 16-bit rows until the SMs' four CTAs are full (1 row 1.7 us,
+    // 592 rows 2.0, against 2.0 and 2.05 with 16 lanes; 4736 rows 3.75 against 3.05), float rows, whose
+    // registers leave 16 lanes three CTAs an SM, up to 8192 (4736 rows 5.0 against 6.1; 20000 rows 18.6 against
+    // 17.8)
+    if (p.T <= (sizeof(T) == 4 ? 8192 : 592)) return go(append_rows_kernel<T, 32, 2, FP8>, 1, 4);
+    return go(append_rows_kernel<T, 16, 4, FP8>, 2, sizeof(T) == 4 ? 3 : 4);
+  }
+  return go(append_rows_kernel<T, 32, 4, FP8>, 1, 3);
 }
 
 cudaError_t launch_append_rows(const mla_dims& d, const void* kv, int64_t kv_ld, int n_tok, const int32_t* seq_idx,

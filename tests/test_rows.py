@@ -118,6 +118,15 @@ def test_norm_rows_count(lib, act, t):
     run_norm(lib, act, t, 1536, seed=t)
 
 
+@pytest.mark.parametrize("act", ACT)
+@pytest.mark.parametrize("width", [72, 1000, 2056, 7168, 8200, 16384])
+@pytest.mark.parametrize("res,gamma,outs", [(True, True, ("sum", "q")), (True, True, ("sum", "y")), (False, True, ("y", "q")),
+                                            (True, False, ("q",)), (False, False, ("sum", "y"))])
+def test_norm_many_rows(lib, act, width, res, gamma, outs):
+    """More rows than CTAs that run at once: each CTA walks several, the last ones a row fewer."""
+    run_norm(lib, act, 1201 if width <= 2056 else 641, width, res=res, gamma=gamma, outs=outs, pad=16, seed=width)
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (1, 0), (0, 1), (24, 8)])
 def test_norm_strides_and_alignment(lib, pad, offset):
     for act in ACT:
@@ -288,6 +297,41 @@ def test_append_rows(lib, act, kind, gamma):
 @pytest.mark.parametrize("lengths", [(1,), (5,), (700, 1, 3)])
 def test_append_rows_counts(lib, act, kind, lengths):
     run_append(lib, act, kind, lengths=lengths, seed=3)
+
+
+@pytest.mark.parametrize("act,kind", KINDS)
+@pytest.mark.parametrize("d_c,d_rope,page,lengths", [(512, 64, 64, (600,)), (512, 128, 16, (1, 5003, 2)), (128, 8, 7, (9000, 4)),
+                                                     (384, 64, 64, (9001,)), (1024, 64, 64, (2000, 1))])
+def test_append_rows_many_tokens(lib, act, kind, d_c, d_rope, page, lengths):
+    """More tokens than run at once, odd counts among them: the last group of a warp has none."""
+    run_append(lib, act, kind, d_c=d_c, d_rope=d_rope, page=page, lengths=lengths, pad=8, seed=4)
+
+
+@pytest.mark.parametrize("act,kind", KINDS)
+def test_append_rows_bad_tokens_among_many(lib, act, kind):
+    n = 9001
+    c = Cache(lib, act, kind, 512, 64, 64, (n, n))
+    seq = (torch.arange(n) % 2).int().cuda()
+    pos = torch.arange(n).int().cuda()
+    bad = torch.tensor([0, 1, 592, 601, 4737, n - 1], device="cuda")
+    good = torch.ones(n, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    at = c.slots(seq, pos)[good]
+    seq[bad[:3]] = 2
+    pos[bad[3:]] = torch.tensor([n, -1, 1 << 30], dtype=torch.int32, device="cuda")
+    kv = randn((n, 576), 6).to(act)
+    cos, sin = rope_tables(lib, 64, n)
+    lib.mla_append_rows(c.dims, kv, 576, n, seq, pos, None, 0.0, cos, sin, n, c.desc)
+    status, detail = lib.mla_check_device_error()
+    assert status == 4 and detail >> 24 in (2, 4)
+    rest = torch.ones(c.pages * 64, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    empty = 99 if kind == "fp8" else GUARD
+    assert (c.rows[rest] == empty).all()
+    if kind == "fp8":
+        check_codes(c.rows[at], c.scales[at], kv[good][:, :512].double(), 512, 2.0 ** -24)
+    else:
+        near(c.rows[at][:, :512], kv[good][:, :512].double(), 0.0)
 
 
 @pytest.mark.parametrize("act,kind", KINDS)
