@@ -23,7 +23,8 @@ using namespace sm100;
 // ------------------------------------------------------------------ any layout
 // fp32 FMA on the CUDA cores: 64 tokens x 64 outputs per CTA, 4 x 4 per thread, 16 values of K at
 // a time.  Every width, alignment and leading dimension; the path of what the tensor-core
-// kernels do not take.
+// kernels do not take (about 22 TFLOP/s; the FMAs, their shared-memory reads and the decoding of the codes
+// bound it).
 template <typename T>
 __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
   __shared__ float xs_s[16][64 + 4];
@@ -87,38 +88,51 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
 // the tokens its N operand (BN columns), and the S CTAs of a cluster each take a range of the
 // scale blocks, so that enough loads are in flight on every SM.  One stage is one scale block:
 // 128 weight rows and BN token rows of 128 bytes, a single row of the 128-byte swizzle.  Each
-// block's products go to a TMEM accumulator of their own (ND of them in turn); the promoting warps
+// block's products go to a TMEM accumulator of their own (ND of them in turn).  One signal a block, the
+// commit of its MMAs, tells the loads that the stage is free and the sums that the products are there; with
+// a signal for each, and waits that were not asked ahead, the issuing warp bound the kernel (680 clocks a
+// block; 64 x 7168 x 16384 28.0 us against 25.8).  The promoting warps
 // (four lane quarters x column groups) read it, scale its columns by xs[t, b] ws[n / 128, b] (made by
 // a warp of its own, XC blocks at a time) and add it to fp32 sums in registers.  At the end each
 // CTA lays its sums out in its idle stage ring and sends every other CTA the rows that one owns, one bulk
 // copy each into a buffer of the owner's shared memory; the owner adds the S partial sums of its rows
 // in rank order and stores them: no workspace, no atomics.
+//
+// 64 x 7168 x 16384: 25.9 us, 4.5 TB/s of weights (their bytes at copy bandwidth: 18.2 us).  56 tiles split in two
+// leave 36 SMs idle, and the start, the exchange and the last sums take some 6 us; 64 x 18944 x 16384, which
+// fills the SMs, reads 5.9 TB/s.  64 x 2112 x 7168: 7.6 us, 1 x 576 x 2048: 3.2 us, the chain of wait, load, MMA,
+// exchange and store.  Tried: 8 promoting warps for 64 columns (42 us against 30 at the time), the exchange by
+// asynchronous 16-byte stores from registers (64 x 2112 x 7168 0.4 us longer than by bulk copies), the next
+// block's products loaded ahead of the sums (nothing: the issuing warp bound the blocks, not these).
 constexpr int A_BYTES = 128 * 128;
 
-template <int BN>
+template <int BN, int OCC>  // OCC: CTAs per SM
 struct SkCfg {
-  static constexpr int OCC = BN <= 32 ? 2 : 1;          // CTAs per SM
-  static constexpr int NST = BN == 16 ? 5 : BN == 64 ? 7 : 4;
+  static constexpr int NST = BN == 128 ? 4 : OCC == 1 ? (BN == 64 ? 7 : 8) : BN == 16 ? 5 : 4;
   static constexpr int STAGE = A_BYTES + BN * 128;
   static constexpr int ND = 4;
   static constexpr uint32_t TCOLS = ND * BN;            // 64 to 512 columns
-  static constexpr int PW = BN <= 32 ? 8 : 16;          // promoting warps: four lane quarters x column groups
+  static constexpr int PW = BN <= 32 || OCC == 2 ? 8 : 16;  // promoting warps: four lane quarters x column groups
   static constexpr int CW = BN / (PW / 4);              // columns of one of them
   static constexpr int XC = 8;                          // scale blocks made at a time
+  static constexpr int SW = BN <= 32 ? 1 : 2;           // warps that make them
   static constexpr int SLD = BN + 4;
-  static constexpr int THREADS = 128 + PW * 32;         // warps 0 TMA, 1 MMA, 2 scales, 4 and up promoting
+  static constexpr int THREADS = 128 + PW * 32;         // warps 0 TMA, 1 MMA, 2 and 3 scales, 4 and up promoting
   static constexpr int SC_OFF = NST * STAGE;            // scales: [2][XC][SLD] fp32
   static constexpr int RLD = BN + 4;                    // floats of a row of partial sums (bank spread)
   static constexpr int RECV_OFF = SC_OFF + 2 * XC * SLD * 4;      // [S][rows of the largest share][RLD]
-  static constexpr int BAR_OFF = RECV_OFF + (128 + 7) * RLD * 4;  // (S ceil(128 / S) is at most 135 for S <= 8)
+  static constexpr bool SPLIT = BN != 64 || OCC == 1;   // 64 columns leave no room for RECV beside a second CTA: S = 1
+  // (S ceil(128 / S) is at most 135 for S <= 8)
+  static constexpr int BAR_OFF = RECV_OFF + (SPLIT ? (128 + 7) * RLD * 4 : 0);
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  static_assert(NST >= ND, "done[] is not signalled again before its block is summed");
   static_assert(128 * RLD * 4 <= NST * STAGE && RECV_OFF % 16 == 0 && BAR_OFF % 8 == 0, "layout");
   static_assert(OCC * (SMEM + 1024) <= 233472 && OCC * TCOLS <= 512, "CTAs per SM");
 };
 
-template <int BN>
+template <int BN, int OCC>
 struct SkBars {
-  uint64_t full[SkCfg<BN>::NST], empty[SkCfg<BN>::NST], dfull[SkCfg<BN>::ND], dempty[SkCfg<BN>::ND];
+  uint64_t full[SkCfg<BN, OCC>::NST], done[SkCfg<BN, OCC>::NST], dempty[SkCfg<BN, OCC>::ND];
   uint64_t sfull[2], sempty[2], received;
   uint32_t tmem_base;
 };
@@ -167,15 +181,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 
-template <int BN>
-__global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
+template <int BN, int OCC>
+__global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
     fp8_skinny_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const SkParams p) {
-  using C = SkCfg<BN>;
+  using C = SkCfg<BN, OCC>;
   extern __shared__ uint8_t smem_raw[];
   // (an offset, not a cast of the rounded address: accesses stay shared-memory ones, not generic)
   uint8_t* smem = smem_raw + ((1024u - smem_addr(smem_raw)) & 1023u);
-  SkBars<BN>* bars = reinterpret_cast<SkBars<BN>*>(smem + C::BAR_OFF);
+  SkBars<BN, OCC>* bars = reinterpret_cast<SkBars<BN, OCC>*>(smem + C::BAR_OFF);
   float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int S = gridDim.x, rank = blockIdx.x;
@@ -192,14 +206,13 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
   if (warp == 2) {  // a lane a barrier
     if (lane < C::NST) {
       mbar_init(&bars->full[lane], 1);
-      mbar_init(&bars->empty[lane], 1);
+      mbar_init(&bars->done[lane], 1);
     }
     if (lane < C::ND) {
-      mbar_init(&bars->dfull[lane], 1);
       mbar_init(&bars->dempty[lane], C::PW);
     }
     if (lane < 2) {
-      mbar_init(&bars->sfull[lane], 1);
+      mbar_init(&bars->sfull[lane], C::SW);
       mbar_init(&bars->sempty[lane], C::PW);
     }
     if (lane == 0) mbar_init(&bars->received, 1);
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < nb; ++i) {
-      if (!warp_wait(&bars->empty[s], ph ^ 1)) {
+      if (!warp_wait(&bars->done[s], ph ^ 1)) {
         if (lane == 0) record_error(p.err, ERR_TIMEOUT, 60);
         break;
       }
@@ -262,9 +275,11 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
     const uint64_t x0 = umma_desc(smem_addr(smem) + A_BYTES, 16, 1024, UMMA_SW128);
     int s = 0;
     uint32_t ph = 0;
+    bool loaded = false, freed = false;  // asked while the block before is issued
     for (int i = 0; i < nb; ++i) {
       const int d = i % C::ND;
-      if (!warp_wait(&bars->dempty[d], ((i / C::ND) & 1) ^ 1) || !warp_wait(&bars->full[s], ph)) {
+      const bool ok = (loaded || mbar_wait(&bars->full[s], ph)) && (freed || mbar_wait(&bars->dempty[d], ((i / C::ND) & 1) ^ 1));
+      if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) record_error(p.err, ERR_TIMEOUT, 61);
         break;
       }
@@ -274,16 +289,17 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_f8(tmem + d * BN, a0 + at + 2 * kk, x0 + at + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-        mma_commit(&bars->empty[s]);
-        mma_commit(&bars->dfull[d]);
+        mma_commit(&bars->done[s]);
       }
       __syncwarp();
       if (++s == C::NST) {
         s = 0;
         ph ^= 1;
       }
+      loaded = mbar_test(&bars->full[s], ph);
+      freed = mbar_test(&bars->dempty[(i + 1) % C::ND], (((i + 1) / C::ND) & 1) ^ 1);
     }
-  } else if (warp == 2) {
+  } else if (warp < 2 + C::SW) {
     // -------------------------------------------------------------- scales of the CTA's tokens
     // Eight lanes read the 32 bytes of a token's chunk.  Past the last token: zero.
     griddep_wait();
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
       const float w = ws[b];
       float* dst = scales + ((c & 1) * C::XC + k) * C::SLD;
 #pragma unroll 1
-      for (int r0 = 0; r0 < BN; r0 += 32) {
+      for (int r0 = (warp - 2) * 32; r0 < BN; r0 += C::SW * 32) {
         float x[C::XC];
 #pragma unroll
         for (int j = 0; j < C::XC; ++j) {
@@ -318,10 +334,12 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
     griddep_wait();
     if (threadIdx.x == 128) griddep_launch_dependents();
     const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + col0;
+    int s = 0;
+    uint32_t ph = 0;
     for (int i = 0; i < nb; ++i) {
       const int c = i / C::XC, d = i % C::ND;
       if ((i % C::XC == 0 && !warp_wait(&bars->sfull[c & 1], (c >> 1) & 1)) ||
-          !warp_wait(&bars->dfull[d], (i / C::ND) & 1)) {
+          !warp_wait(&bars->done[s], ph)) {
         if (lane == 0) record_error(p.err, ERR_TIMEOUT, 62);
         break;
       }
@@ -347,6 +365,10 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
           s0 = fma2(pack2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])), x.x, s0);
           s1 = fma2(pack2(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3])), x.y, s1);
         }
+      }
+      if (++s == C::NST) {
+        s = 0;
+        ph ^= 1;
       }
       if (i % C::XC == C::XC - 1) {  // (the CTA's last chunk is not written again)
         __syncwarp();
@@ -382,17 +404,30 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
     __syncthreads();
     recv = part;
   }
-  // ---- sums of this CTA's rows: a lane takes a row, a warp a token at a time
-  if (ok)
+  // ---- sums of this CTA's rows: a thread takes four tokens of a row, neighbouring lanes neighbouring rows
+  if (ok) {
+    const int shift = rows <= 16 ? 4 : rows <= 32 ? 5 : rows <= 64 ? 6 : 7;
 #pragma unroll 1
-    for (int c = warp; c < BN && t0 + c < p.T; c += C::THREADS / 32)
-#pragma unroll 1
-      for (int m = lane; m < rows && n0 + lo + m < p.N; m += 32) {
-        float v = 0.f;
-#pragma unroll 2
-        for (int r = 0; r < S; ++r) v += recv[(r * share + m) * C::RLD + c];
-        store_out(p, t0 + c, n0 + lo + m, v);
+    for (int e = threadIdx.x; e < (BN / 4) << shift; e += C::THREADS) {
+      const int m = e & ((1 << shift) - 1), c = (e >> shift) * 4;
+      if (m >= rows || n0 + lo + m >= p.N || t0 + c >= p.T) continue;
+      float4 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        v[r] = r < S ? *reinterpret_cast<const float4*>(recv + (r * share + m) * C::RLD + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 1; r < 8; ++r) {  // (in rank order; those past S add zeros)
+        v[0].x += v[r].x;
+        v[0].y += v[r].y;
+        v[0].z += v[r].z;
+        v[0].w += v[r].w;
       }
+      const float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + c + i < p.T) store_out(p, t0 + c + i, n0 + lo + m, sum[i]);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -409,9 +444,14 @@ __global__ void __launch_bounds__(SkCfg<BN>::THREADS, SkCfg<BN>::OCC)
 // K = 32, four per block) leaves 128 tokens x WN outputs in each CTA's TMEM.  Here the tokens are the
 // lanes, so a thread scales its columns by one or two numbers per block, xs[t, b] ws[n / 128, b].  Eight
 // promoting warps (four lane quarters x two column halves) keep WN / 2 fp32 sums a thread while
-// the next block's MMA fills the other accumulator.  Two more warps compute the scales some blocks
+// the next blocks' MMAs fill the other accumulators.  Two more warps compute the scales some blocks
 // ahead.  Persistent over tiles; a finished tile goes out through 4 KB of shared memory a warp and
 // TMA stores.
+//
+// 2048 x 7168 x 16384: 233 us, 2.06 PFLOP/s (a long loop of them runs at the power cap, 275 us).  A block of 160
+// outputs takes a pair 0.307 us, of 128 0.26; the MMAs alone need 0.215 for 128 outputs and 0.29 for 256 (an MMA
+// of N = 128 runs at two thirds of N = 256's rate).  What it waits for is the sums: 256 outputs leave TMEM room for two
+// accumulators only, and the tensor pipe idles while one is read (0.56 us a block); 192 outputs 0.42.
 template <int WN>
 struct WdCfg {
   static constexpr int HC = WN / 2;                    // columns of a promoting warp
@@ -427,7 +467,7 @@ struct WdCfg {
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
   // warpgroup 0: TMA, MMA and two scale warps; warpgroups 1 and 2: the promoting warps, which hold WN / 2
   // sums and as many loaded values a thread.  Registers at launch 384 x 168 = 64512, after the split
-  // 128 x 80 + 256 x 208 = 63488.
+  // 128 x 72 + 256 x 216 = 64512.
   static constexpr int THREADS = 384;
   static constexpr int REGS_FEW = 72, REGS_MANY = 216;
   static_assert((TAIL == 0 || TAIL == 16) && STAGE % 1024 == 0 && SMEM <= 232448, "shared memory of one CTA per SM");
@@ -802,15 +842,15 @@ static bool map_bytes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t 
 
 // Clusters of S CTAs of the kernel that the device holds at once (they do not span its GPCs, so it
 // is less than its SMs over S).  Looked up once per device and size.
-template <int BN>
+template <int BN, int OCC>
 static int skinny_clusters(int S) {
-  using C = p8::SkCfg<BN>;
+  using C = p8::SkCfg<BN, OCC>;
   static std::atomic<int> known[64][9];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = known[dev][S].load(std::memory_order_relaxed);
   if (n) return n - 1;
-  if (cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+  if (cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN, OCC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S);
@@ -823,7 +863,7 @@ static int skinny_clusters(int S) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, p8::fp8_skinny_kernel<BN>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, p8::fp8_skinny_kernel<BN, OCC>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -833,25 +873,25 @@ static int skinny_clusters(int S) {
 
 // CTAs per tile of the few-token kernel: the most that still run all at once, with two scale
 // blocks each at least.
-template <int BN>
+template <int BN, int OCC>
 static int skinny_split(const Fp8Args& a) {
   const int blocks = (a.K + 127) / 128;
   const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
   int S = 1;
-  for (int s = 2; s <= 8 && 2 * s <= blocks; ++s)
-    if (tiles <= skinny_clusters<BN>(s)) S = s;
+  for (int s = 2; p8::SkCfg<BN, OCC>::SPLIT && s <= 8 && 2 * s <= blocks; ++s)
+    if (tiles <= skinny_clusters<BN, OCC>(s)) S = s;
   return S;
 }
 
-template <int BN>
+template <int BN, int OCC>
 static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
-  using C = p8::SkCfg<BN>;
+  using C = p8::SkCfg<BN, OCC>;
   CUtensorMap mw, mx;
   if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN)) return kUnsupported;
   const int blocks = (a.K + 127) / 128, tiles_n = (a.N + 127) / 128;
   const long tiles_t = (a.T + BN - 1) / BN;
   if (tiles_t > 65535 || tiles_n > 65535) return kUnsupported;
-  const int S = skinny_split<BN>(a);
+  const int S = skinny_split<BN, OCC>(a);
   p8::SkParams p;
   p.xs = a.xs;
   p.ws = a.ws;
@@ -863,7 +903,7 @@ static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
   p.out_ld = a.out_ld;
   p.out_f32 = a.act == MLA_F32;
   p.err = a.err;
-  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN, OCC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, (unsigned)tiles_t);
@@ -879,7 +919,7 @@ static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, p8::fp8_skinny_kernel<BN>, mw, mx, p);
+  e = cudaLaunchKernelEx(&cfg, p8::fp8_skinny_kernel<BN, OCC>, mw, mx, p);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -968,36 +1008,58 @@ static bool tma_layout(const Fp8Args& a) {
          a.x_ld % 16 == 0;
 }
 
-// Which kernel: up to 32 tokens the few-token one (the weights' bytes decide, and 16 or 32 columns keep
-// two CTAs on an SM).  Above, the variant with the least time by these models of what was measured on
-// B200 (us; a wave is one round of the CTAs or pairs that run at once):
-//   few tokens, 64 columns    waves (0.385 blocks per CTA + 4) + 1.5    64x7168x16384: 29 (many-token: 43)
-//   few tokens, 128 columns   waves (0.40 blocks per CTA + 7) + 1.5     128x7168x16384: 36 (64 columns: 50)
-//   many tokens, 128 outputs  waves (0.26 blocks + 0.75) + 4            256x7168x16384: 40 (few-token: 60)
-//   many tokens, 160 outputs  waves (0.307 blocks + 1.3) + 4            2048x7168x16384: 240 (128 outputs: 290)
+// Up to 32 columns the few-token kernel comes with two CTAs per SM or with one and a deeper ring (us at 1 and
+// 32 tokens, two / one per SM; a range of K per CTA that is long streams faster from fewer CTAs):
+//   7168x16384 (64 blocks per CTA with one per SM)   24.1, 27.1 / 21.9, 23.5
+//   4096x7168 (14)                                    7.0, 7.9 / 7.0, 7.7
+//   2112x7168 (8)                                     5.4, 6.0 / 5.6, 6.1
+//   24576x1536 (12, but two waves)                    8.9, 10.3 / 12.0, 13.5
+template <int BN>
+static cudaError_t launch_narrow(const Fp8Args& a, cudaStream_t st) {
+  const int blocks = (a.K + 127) / 128, S = skinny_split<BN, 1>(a);
+  const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
+  return tiles <= 148 && (blocks + S - 1) / S >= 16 ? launch_skinny<BN, 1>(a, st) : launch_skinny<BN, 2>(a, st);
+}
+
+// Which kernel: up to 32 tokens the few-token one (the weights' bytes decide).  Above, the variant with the
+// least time by these models of what was measured on B200 (us; a wave is one round of the CTAs or pairs that
+// run at once):
+//   few tokens, 32 columns    0.3 blocks per CTA + 3.2, the blocks at 0.6 where SMs hold two CTAs
+//                                                          64x576x2048: 3.8 (64 columns: 4.8), 64x2112x7168: 8.4 (7.5)
+//   few tokens, 64 columns    waves (0.335 blocks per CTA + 3.2) + 1.5   64x7168x16384: 26 (many-token: 43)
+//     with two CTAs per SM, unsplit                        64x24576x1536: 13 (one: 16), 64x14336x2048: 10.7 (9.8)
+//   few tokens, 128 columns   waves (0.39 blocks per CTA + 6.8) + 1.5    128x7168x16384: 33 (64 columns: 50)
+//   many tokens, 128 outputs  waves (0.26 blocks + 0.75) + 2.8           256x7168x16384: 38 (few-token: 58)
+//   many tokens, 160 outputs  waves (0.307 blocks + 1.3) + 2.8           2048x7168x16384: 240 (128 outputs: 290)
 // and 3.5 more a wave of the many-token kernel whose output rows TMA stores do not take
 // (333x1999x2000: 12.6, few-token 10.4).
-template <int BN>
+template <int BN, int OCC>
 static float skinny_us(const Fp8Args& a, float block, float wave) {
-  const int blocks = (a.K + 127) / 128, S = skinny_split<BN>(a);
+  const int blocks = (a.K + 127) / 128, S = skinny_split<BN, OCC>(a);
   const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
-  const long waves = S > 1 ? 1 : (tiles + 147) / 148;
-  return waves * (block * ((blocks + S - 1) / S) + wave) + 1.5f;
+  const long waves = S > 1 ? 1 : (tiles + 148 * OCC - 1) / (148 * OCC);
+  return waves * (block * (tiles * S > 148 ? OCC : 1) * ((blocks + S - 1) / S) + wave) + 1.5f;
 }
 static float wide_us(const Fp8Args& a, int wn, float block, float wave) {
   const long tiles = (long)((a.N + wn - 1) / wn) * ((a.T + 255) / 256);
-  return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave + (out_aligned(a) ? 0.f : 3.5f)) + 4.f;
+  return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave + (out_aligned(a) ? 0.f : 3.5f)) + 2.8f;
 }
 
 cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
   if (!tma_layout(a)) return launch_fp8_any(a, st);
-  if (a.T <= 16) return launch_skinny<16>(a, st);
-  if (a.T <= 32) return launch_skinny<32>(a, st);
+  if (a.T <= 16) return launch_narrow<16>(a, st);
+  if (a.T <= 32) return launch_narrow<32>(a, st);
   const float w128 = wide_us(a, 128, 0.26f, 0.75f), w160 = wide_us(a, 160, 0.307f, 1.3f);
   if (a.T <= 1024) {
-    const float s64 = skinny_us<64>(a, 0.385f, 4.f);
-    const float s128 = a.T > 64 ? skinny_us<128>(a, 0.40f, 7.f) : s64 + 1.f;
-    if (fminf(s64, s128) < fminf(w128, w160)) return s64 <= s128 ? launch_skinny<64>(a, st) : launch_skinny<128>(a, st);
+    const float s32 = a.T <= 128 ? skinny_us<32, 2>(a, 0.3f, 1.7f) : 1e30f;
+    const float s64 = skinny_us<64, 1>(a, 0.335f, 3.2f), s64x2 = skinny_us<64, 2>(a, 0.335f, 3.2f);
+    const float s128 = a.T > 64 ? skinny_us<128, 1>(a, 0.39f, 6.8f) : 1e30f;
+    const float least = fminf(fminf(s32, s64), fminf(s64x2, s128));
+    if (least < fminf(w128, w160))
+      return least == s32     ? launch_skinny<32, 2>(a, st)
+             : least == s64   ? launch_skinny<64, 1>(a, st)
+             : least == s64x2 ? launch_skinny<64, 2>(a, st)
+                              : launch_skinny<128, 1>(a, st);
   }
   return w128 < w160 ? launch_wide<128>(a, st) : launch_wide<160>(a, st);
 }

@@ -99,6 +99,16 @@ def test_larger(lib, act, t, n, k):
     run(lib, t, n, k, act, seed=7)
 
 
+# few tokens: two token tiles, long ranges of the width per block of threads (split and not), more output tiles
+# than streaming multiprocessors, and two of them on one
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t,n,k", [(50, 576, 2048), (128, 570, 1040), (5, 18810, 2064), (32, 18810, 2064), (3, 9400, 4112),
+                                   (30, 7000, 4112), (16, 24576, 400), (31, 19330, 272), (64, 24570, 400), (33, 19100, 1040),
+                                   (100, 9500, 512), (64, 1100, 4112), (128, 1100, 4112)])
+def test_few_rows_many_outputs(lib, act, t, n, k):
+    run(lib, t, n, k, act, seed=9)
+
+
 @pytest.mark.parametrize("out_pad", [1, 3, 7, 8])
 def test_output_rows_apart(lib, out_pad):
     for t in (7, 300):
