@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(RW_WARPS * 32) rows_warp_kernel(const RowsArgs
 // ------------------------------------------------------------------ norm of many rows
 // A CTA walks rows blockIdx, blockIdx + gridDim, ... with a ring of rows in shared memory that bulk
 // copies fill ahead of it, so loads are in flight through the barriers, sums and stores of a row (the
-// kernel above, a row per CTA, takes 129 us for 8191 x 7168 with the residual, this one 87: 5.4
+// kernel above, a row per CTA, takes 129 us for 8191 x 7168 with the residual, this one 87: 6.1
 // TB/s).  A stage holds a row of x and, after it, the residual's; it is refilled once
 // every thread has its values in registers, which the barrier of the row's sum shows.
 constexpr int RS_MAX_STAGES = 8;
@@ -592,7 +592,7 @@ constexpr int AR_WARPS = 4;
 // lanes walks tokens w, w + (groups of the grid), ... with the next token's row and its page id (whose
 // position came one token earlier still) under way; a token a warp waited for each of these in turn.
 // With 16 lanes a warp's instructions serve two tokens, and these kernels issue for half of their time.
-// 40007 bf16 tokens of 512 + 64: 18.7 us, 4.9 TB/s (32 lanes 21.2; without the prefetch 25), into the
+// 40007 bf16 tokens of 512 + 64: 18.7 us, 5.5 TB/s (32 lanes 21.2; without the prefetch 25), into the
 // 8-bit cache 19.1 (22.8).
 template <typename T, int LANES, int CH, bool FP8>
 __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const AppendParams p) {
