@@ -38,8 +38,8 @@
  *     they read, and everything they write, comes after the wait.  So a weight (or query
  *     input) must not be an output of the immediately preceding library call on the same
  *     stream.  (Calls before that one have completed: a kernel lets the next one start only
- *     after its own wait.)  One exception: q_nope may come from mla_project_fp8 directly in front,
- *     called by the same host thread; mla_absorb_query is then launched normally.
+ *     after its own wait.)  One exception: q_nope may come from mla_project_fp8 or mla_norm_rows
+ *     directly in front, called by the same host thread; mla_absorb_query is then launched normally.
  *     Setting MLA_PDL=0 in the environment (read once) launches them all normally.
  */
 #ifndef MLA_H_

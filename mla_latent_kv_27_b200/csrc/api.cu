@@ -84,19 +84,19 @@ bool pdl_enabled() {
   return on;
 }
 
-// The calling thread's latest call that enqueued work: its stream, and whether it was the 8-bit
-// projection.  The absorb kernel reads q_nope before it waits for the kernel in front of it, so it is
-// launched without programmatic overlap unless that kernel is known to be another call of this
-// library: the projection may have written q_nope.  (Only the kernel directly in front matters:
+// The calling thread's latest call that enqueued work: its stream, and whether its rows may be a q_nope
+// (the 8-bit projection's and the norm's may).  The absorb kernel reads q_nope before it waits for the
+// kernel in front of it, so it is launched without programmatic overlap unless that kernel is known to be a
+// call of this library that cannot have written q_nope.  (Only the kernel directly in front matters:
 // every kernel lets the next one start after its own wait, when all before it have completed.)
 static thread_local const void* t_stream = nullptr;
-static thread_local bool t_known = false, t_projected = false;
-static void note_call(const void* stream, bool projected = false) {
+static thread_local bool t_known = false, t_rows = false;
+static void note_call(const void* stream, bool rows = false) {
   t_stream = stream;
   t_known = true;
-  t_projected = projected;
+  t_rows = rows;
 }
-static bool absorb_may_overlap(const void* stream) { return t_known && t_stream == stream && !t_projected; }
+static bool absorb_may_overlap(const void* stream) { return t_known && t_stream == stream && !t_rows; }
 
 static mla_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
@@ -340,7 +340,7 @@ mla_status mla_norm_rows(int32_t act_dtype, const void* x, int64_t x_ld, const v
   if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, residual, residual_ld, gamma, n_tok, width, eps,
                       sum_out, sum_ld, y, y_ld, codes, codes_ld, scales, err};
-  note_call(stream);
+  note_call(stream, sum_out || y);
   return cuda_status(launch_rows(a, true, static_cast<cudaStream_t>(stream)));
 }
 

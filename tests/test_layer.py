@@ -159,3 +159,29 @@ def test_absorb_directly_behind_the_projection(lib, between):
         project_and_absorb(torch.cuda.synchronize)
         torch.cuda.synchronize()
         assert torch.equal(got, L.q_packed)
+
+
+@pytest.mark.gpu
+def test_absorb_directly_behind_the_norm(lib):
+    """The same with q_nope normed in place by mla_norm_rows directly in front."""
+    from mla_latent_kv_27_b200.runner import MLALayer
+    w = dataclasses.replace(W["v3_bf16"], d_model=512)
+    L = MLALayer(w, 1536, lengths=(130,) * 40)
+    L.draw_step_inputs()
+    rows, d = L.n_tok * w.n_heads, w.d_nope
+    q = L.q_nope.clone()
+    g = torch.linspace(0.5, 2, d, device="cuda").bfloat16()
+
+    def norm_and_absorb(wait):
+        L.q_nope.copy_(q)
+        torch.cuda.synchronize()
+        lib.mla_norm_rows(L.act, L.q_nope, d, None, 0, g, rows, d, 1e-6, None, 0, L.q_nope, d, None, 0, None)
+        wait()
+        L.absorb()
+        torch.cuda.synchronize()
+        return L.q_packed.clone()
+
+    want = norm_and_absorb(torch.cuda.synchronize)
+    L.q_packed.zero_()
+    for _ in range(6):
+        assert torch.equal(norm_and_absorb(lambda: None), want)
