@@ -840,18 +840,26 @@ static bool map_bytes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of S CTAs of the kernel that the device holds at once (they do not span its GPCs, so it
-// is less than its SMs over S).  Looked up once per device and size.
+// What is looked up or set once per device: the few-token kernel's shared memory, and how many clusters
+// of S of its CTAs the device holds at once (they do not span its GPCs, so it is less than its SMs over S).
 template <int BN, int OCC>
-static int skinny_clusters(int S) {
+static cudaError_t skinny_ready(int dev) {
+  using C = p8::SkCfg<BN, OCC>;
+  static std::atomic<bool> set[64];
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN, OCC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e == cudaSuccess) set[dev].store(true, std::memory_order_release);
+  return e;
+}
+template <int BN, int OCC>
+static int skinny_clusters(int dev, int S) {
   using C = p8::SkCfg<BN, OCC>;
   static std::atomic<int> known[64][9];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (dev < 0 || dev >= 64) return 0;
   int n = known[dev][S].load(std::memory_order_relaxed);
   if (n) return n - 1;
-  if (cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN, OCC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return 0;
+  if (skinny_ready<BN, OCC>(dev) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S);
   cfg.blockDim = dim3(C::THREADS);
@@ -874,24 +882,23 @@ static int skinny_clusters(int S) {
 // CTAs per tile of the few-token kernel: the most that still run all at once, with two scale
 // blocks each at least.
 template <int BN, int OCC>
-static int skinny_split(const Fp8Args& a) {
+static int skinny_split(const Fp8Args& a, int dev) {
   const int blocks = (a.K + 127) / 128;
   const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
-  int S = 1;
-  for (int s = 2; p8::SkCfg<BN, OCC>::SPLIT && s <= 8 && 2 * s <= blocks; ++s)
-    if (tiles <= skinny_clusters<BN, OCC>(s)) S = s;
-  return S;
+  if (p8::SkCfg<BN, OCC>::SPLIT)
+    for (int s = min(8, blocks / 2); s >= 2; --s)
+      if (tiles * s <= 148 * OCC && tiles <= skinny_clusters<BN, OCC>(dev, s)) return s;
+  return 1;
 }
 
 template <int BN, int OCC>
-static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
+static cudaError_t launch_skinny(const Fp8Args& a, int dev, int S, cudaStream_t st) {
   using C = p8::SkCfg<BN, OCC>;
   CUtensorMap mw, mx;
   if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN)) return kUnsupported;
   const int blocks = (a.K + 127) / 128, tiles_n = (a.N + 127) / 128;
   const long tiles_t = (a.T + BN - 1) / BN;
   if (tiles_t > 65535 || tiles_n > 65535) return kUnsupported;
-  const int S = skinny_split<BN, OCC>(a);
   p8::SkParams p;
   p.xs = a.xs;
   p.ws = a.ws;
@@ -903,7 +910,7 @@ static cudaError_t launch_skinny(const Fp8Args& a, cudaStream_t st) {
   p.out_ld = a.out_ld;
   p.out_f32 = a.act == MLA_F32;
   p.err = a.err;
-  cudaError_t e = cudaFuncSetAttribute(p8::fp8_skinny_kernel<BN, OCC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = skinny_ready<BN, OCC>(dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, (unsigned)tiles_t);
@@ -1015,10 +1022,11 @@ static bool tma_layout(const Fp8Args& a) {
 //   2112x7168 (8)                                     5.4, 6.0 / 5.6, 6.1
 //   24576x1536 (12, but two waves)                    8.9, 10.3 / 12.0, 13.5
 template <int BN>
-static cudaError_t launch_narrow(const Fp8Args& a, cudaStream_t st) {
-  const int blocks = (a.K + 127) / 128, S = skinny_split<BN, 1>(a);
+static cudaError_t launch_narrow(const Fp8Args& a, int dev, cudaStream_t st) {
+  const int blocks = (a.K + 127) / 128, S = skinny_split<BN, 1>(a, dev);
   const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
-  return tiles <= 148 && (blocks + S - 1) / S >= 16 ? launch_skinny<BN, 1>(a, st) : launch_skinny<BN, 2>(a, st);
+  if (tiles <= 148 && (blocks + S - 1) / S >= 16) return launch_skinny<BN, 1>(a, dev, S, st);
+  return launch_skinny<BN, 2>(a, dev, skinny_split<BN, 2>(a, dev), st);
 }
 
 // Which kernel: up to 32 tokens the few-token one (the weights' bytes decide).  Above, the variant with the
@@ -1034,8 +1042,8 @@ static cudaError_t launch_narrow(const Fp8Args& a, cudaStream_t st) {
 // and 3.5 more a wave of the many-token kernel whose output rows TMA stores do not take
 // (333x1999x2000: 12.6, few-token 10.4).
 template <int BN, int OCC>
-static float skinny_us(const Fp8Args& a, float block, float wave) {
-  const int blocks = (a.K + 127) / 128, S = skinny_split<BN, OCC>(a);
+static float skinny_us(const Fp8Args& a, int S, float block, float wave) {
+  const int blocks = (a.K + 127) / 128;
   const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
   const long waves = S > 1 ? 1 : (tiles + 148 * OCC - 1) / (148 * OCC);
   return waves * (block * (tiles * S > 148 ? OCC : 1) * ((blocks + S - 1) / S) + wave) + 1.5f;
@@ -1047,19 +1055,23 @@ static float wide_us(const Fp8Args& a, int wn, float block, float wave) {
 
 cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
   if (!tma_layout(a)) return launch_fp8_any(a, st);
-  if (a.T <= 16) return launch_narrow<16>(a, st);
-  if (a.T <= 32) return launch_narrow<32>(a, st);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (a.T <= 16) return launch_narrow<16>(a, dev, st);
+  if (a.T <= 32) return launch_narrow<32>(a, dev, st);
   const float w128 = wide_us(a, 128, 0.26f, 0.75f), w160 = wide_us(a, 160, 0.307f, 1.3f);
   if (a.T <= 1024) {
-    const float s32 = a.T <= 128 ? skinny_us<32, 2>(a, 0.3f, 1.7f) : 1e30f;
-    const float s64 = skinny_us<64, 1>(a, 0.335f, 3.2f), s64x2 = skinny_us<64, 2>(a, 0.335f, 3.2f);
-    const float s128 = a.T > 64 ? skinny_us<128, 1>(a, 0.39f, 6.8f) : 1e30f;
+    const int S32 = skinny_split<32, 2>(a, dev), S64 = skinny_split<64, 1>(a, dev), S128 = skinny_split<128, 1>(a, dev);
+    const float s32 = a.T <= 128 ? skinny_us<32, 2>(a, S32, 0.3f, 1.7f) : 1e30f;
+    const float s64 = skinny_us<64, 1>(a, S64, 0.335f, 3.2f), s64x2 = skinny_us<64, 2>(a, 1, 0.335f, 3.2f);
+    const float s128 = a.T > 64 ? skinny_us<128, 1>(a, S128, 0.39f, 6.8f) : 1e30f;
     const float least = fminf(fminf(s32, s64), fminf(s64x2, s128));
     if (least < fminf(w128, w160))
-      return least == s32     ? launch_skinny<32, 2>(a, st)
-             : least == s64   ? launch_skinny<64, 1>(a, st)
-             : least == s64x2 ? launch_skinny<64, 2>(a, st)
-                              : launch_skinny<128, 1>(a, st);
+      return least == s32     ? launch_skinny<32, 2>(a, dev, S32, st)
+             : least == s64   ? launch_skinny<64, 1>(a, dev, S64, st)
+             : least == s64x2 ? launch_skinny<64, 2>(a, dev, 1, st)
+                              : launch_skinny<128, 1>(a, dev, S128, st);
   }
   return w128 < w160 ? launch_wide<128>(a, st) : launch_wide<160>(a, st);
 }
