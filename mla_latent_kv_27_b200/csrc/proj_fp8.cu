@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
 // a signal for each, and waits that were not asked ahead, the issuing warp bound the kernel (680 clocks a
 // block; 64 x 7168 x 16384 28.0 us against 25.8).  The promoting warps
 // (four lane quarters x column groups) read it, scale its columns by xs[t, b] ws[n / 128, b] (made by
-// a warp of its own, XC blocks at a time) and add it to fp32 sums in registers.  At the end each
+// a warp of its own, XC blocks at a time) and add it to fp32 sums in registers.  At the end, unless unsplit, each
 // CTA lays its sums out in its idle stage ring and sends every other CTA the rows that one owns, one bulk
 // copy each into a buffer of the owner's shared memory; the owner adds the S partial sums of its rows
 // in rank order and stores them: no workspace, no atomics.
@@ -147,11 +147,11 @@ struct SkParams {
   int* err;
 };
 
-__device__ __forceinline__ void store_out(const SkParams& p, long t, int n, float v) {
+__device__ __forceinline__ void store_out(const SkParams& p, long at, float v) {
   if (p.out_f32)
-    static_cast<float*>(p.out)[t * p.out_ld + n] = v;
+    static_cast<float*>(p.out)[at] = v;
   else
-    static_cast<__nv_bfloat16*>(p.out)[t * p.out_ld + n] = __float2bfloat16_rn(v);
+    static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
 }
 // (relaxed: the barriers' initialisation is published by its own fence and data by mbarriers; a release would
 // wait for every store of the thread, about 1 us here)
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
   SkBars<BN, OCC>* bars = reinterpret_cast<SkBars<BN, OCC>*>(smem + C::BAR_OFF);
   float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int S = gridDim.x, rank = blockIdx.x;
+  const int S = C::SPLIT ? gridDim.x : 1, rank = C::SPLIT ? blockIdx.x : 0;
   const int n0 = blockIdx.y * 128;
   const int t0 = blockIdx.z * BN;
   const int b0 = rank * p.per_cta;
@@ -377,38 +377,45 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
     }
   }
 
-  // ---- partial sums [128 rows][RLD] over this CTA's own ring, idle since its last MMA completed
-  float* part = reinterpret_cast<float*>(smem);
-  float* recv = reinterpret_cast<float*>(smem + C::RECV_OFF);
   __syncwarp();
-  if (S > 1) cluster_wait();  // (every CTA of the cluster has begun)
-  if (warp >= 4) {
-    float* dst = part + (quarter * 32 + lane) * C::RLD + col0;
+  if (S == 1) {
+    // ---- unsplit: a warp's lanes are 32 neighbouring outputs of a token, stored from its registers
+    const int n = n0 + quarter * 32 + lane;
+    const int left = warp >= 4 && n < p.N ? p.T - t0 - col0 : 0;  // tokens of this thread
+    long at = (long)(t0 + col0) * p.out_ld + n;
 #pragma unroll
-    for (int c = 0; c < C::CW; c += 4)
-      *reinterpret_cast<ulonglong2*>(dst + c) = make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
-    fence_proxy_async_smem();
-    named_bar_sync(1, C::PW * 32);
-    if (S > 1 && warp == 4 && lane < S) {
-      const int first = lane * 128 / S, n = (lane + 1) * 128 / S - first;
-      bulk_copy_s2cluster(map_to_rank(recv + rank * share * C::RLD, lane), smem_addr(part + first * C::RLD),
-                          (uint32_t)(n * C::RLD * 4), map_to_rank(&bars->received, lane));
+    for (int c = 0; c < C::CW; c += 2) {
+      float v[2];
+      unpack2(acc[c / 2], v[0], v[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i, at += p.out_ld)
+        if (c + i < left) store_out(p, at, v[i]);
     }
-  }
-  bool ok = true;
-  if (S > 1) {
-    ok = warp_wait(&bars->received, 0);
+  } else {
+    // ---- partial sums [128 rows][RLD] over this CTA's own ring, idle since its last MMA completed
+    float* part = reinterpret_cast<float*>(smem);
+    float* recv = reinterpret_cast<float*>(smem + C::RECV_OFF);
+    cluster_wait();  // (every CTA of the cluster has begun)
+    if (warp >= 4) {
+      float* dst = part + (quarter * 32 + lane) * C::RLD + col0;
+#pragma unroll
+      for (int c = 0; c < C::CW; c += 4)
+        *reinterpret_cast<ulonglong2*>(dst + c) = make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
+      fence_proxy_async_smem();
+      named_bar_sync(1, C::PW * 32);
+      if (warp == 4 && lane < S) {
+        const int first = lane * 128 / S, n = (lane + 1) * 128 / S - first;
+        bulk_copy_s2cluster(map_to_rank(recv + rank * share * C::RLD, lane), smem_addr(part + first * C::RLD),
+                            (uint32_t)(n * C::RLD * 4), map_to_rank(&bars->received, lane));
+      }
+    }
+    const bool ok = warp_wait(&bars->received, 0);
     if (!ok && lane == 0) record_error(p.err, ERR_TIMEOUT, 68);
     cluster_arrive();  // this CTA has all that was sent to it
-  } else {
-    __syncthreads();
-    recv = part;
-  }
-  // ---- sums of this CTA's rows: a thread takes four tokens of a row, neighbouring lanes neighbouring rows
-  if (ok) {
-    const int shift = rows <= 16 ? 4 : rows <= 32 ? 5 : rows <= 64 ? 6 : 7;
+    // ---- sums of this CTA's rows: a thread takes four tokens of a row, neighbouring lanes neighbouring rows
+    const int shift = rows <= 16 ? 4 : rows <= 32 ? 5 : 6;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < (BN / 4) << shift; e += C::THREADS) {
+    for (int e = threadIdx.x; ok && e < (BN / 4) << shift; e += C::THREADS) {
       const int m = e & ((1 << shift) - 1), c = (e >> shift) * 4;
       if (m >= rows || n0 + lo + m >= p.N || t0 + c >= p.T) continue;
       float4 v[8];
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
       const float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (t0 + c + i < p.T) store_out(p, t0 + c + i, n0 + lo + m, sum[i]);
+        if (t0 + c + i < p.T) store_out(p, (long)(t0 + c + i) * p.out_ld + n0 + lo + m, sum[i]);
     }
   }
   tc_fence_before();
@@ -1031,22 +1038,25 @@ static cudaError_t launch_narrow(const Fp8Args& a, int dev, cudaStream_t st) {
 
 // Which kernel: up to 32 tokens the few-token one (the weights' bytes decide).  Above, the variant with the
 // least time by these models of what was measured on B200 (us; a wave is one round of the CTAs or pairs that
-// run at once):
-//   few tokens, 32 columns    0.3 blocks per CTA + 3.2, the blocks at 0.6 where SMs hold two CTAs
+// run at once; "+ x if split" is the exchange):
+//   few tokens, 32 columns    0.3 blocks per CTA + 2.7, + 0.5 if split, the blocks at 0.6 where SMs hold two CTAs
 //                                                          64x576x2048: 3.8 (64 columns: 4.8), 64x2112x7168: 8.4 (7.5)
-//   few tokens, 64 columns    waves (0.335 blocks per CTA + 3.2) + 1.5   64x7168x16384: 26 (many-token: 43)
-//     with two CTAs per SM, unsplit                        64x24576x1536: 13 (one: 16), 64x14336x2048: 10.7 (9.8)
-//   few tokens, 128 columns   waves (0.39 blocks per CTA + 6.8) + 1.5    128x7168x16384: 33 (64 columns: 50)
+//   few tokens, 64 columns    waves (0.335 blocks per CTA + 1.8, + 1.4 if split) + 1.5
+//                                                          64x7168x16384: 26 (many-token: 43), 64x14336x2048: 8.7
+//     with two CTAs per SM, unsplit, for more tiles than SMs: waves (0.53 blocks + 2.2) + 1.5
+//                                                          64x24576x1536: 11.2 (one CTA: 16), 64x24576x7168: 33 (49)
+//   few tokens, 128 columns   waves (0.39 blocks per CTA + 5.4, + 1.4 if split) + 1.5
+//                                                          128x7168x16384: 33 (64 columns: 50)
 //   many tokens, 128 outputs  waves (0.26 blocks + 0.75) + 2.8           256x7168x16384: 38 (few-token: 58)
-//   many tokens, 160 outputs  waves (0.307 blocks + 1.3) + 2.8           2048x7168x16384: 240 (128 outputs: 290)
+//   many tokens, 160 outputs  waves (0.307 blocks + 2) + 2.8             2048x7168x16384: 233 (128 outputs: 290)
 // and 3.5 more a wave of the many-token kernel whose output rows TMA stores do not take
-// (333x1999x2000: 12.6, few-token 10.4).
+// (333x1999x2000: 12.6, few-token 9).
 template <int BN, int OCC>
-static float skinny_us(const Fp8Args& a, int S, float block, float wave) {
+static float skinny_us(const Fp8Args& a, int S, float block, float wave, float exchange) {
   const int blocks = (a.K + 127) / 128;
   const long tiles = (long)((a.N + 127) / 128) * ((a.T + BN - 1) / BN);
   const long waves = S > 1 ? 1 : (tiles + 148 * OCC - 1) / (148 * OCC);
-  return waves * (block * (tiles * S > 148 ? OCC : 1) * ((blocks + S - 1) / S) + wave) + 1.5f;
+  return waves * (block * (tiles * S > 148 ? OCC : 1) * ((blocks + S - 1) / S) + wave + (S > 1 ? exchange : 0.f)) + 1.5f;
 }
 static float wide_us(const Fp8Args& a, int wn, float block, float wave) {
   const long tiles = (long)((a.N + wn - 1) / wn) * ((a.T + 255) / 256);
@@ -1060,12 +1070,14 @@ cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (a.T <= 16) return launch_narrow<16>(a, dev, st);
   if (a.T <= 32) return launch_narrow<32>(a, dev, st);
-  const float w128 = wide_us(a, 128, 0.26f, 0.75f), w160 = wide_us(a, 160, 0.307f, 1.3f);
+  const float w128 = wide_us(a, 128, 0.26f, 0.75f), w160 = wide_us(a, 160, 0.307f, 2.f);
   if (a.T <= 1024) {
     const int S32 = skinny_split<32, 2>(a, dev), S64 = skinny_split<64, 1>(a, dev), S128 = skinny_split<128, 1>(a, dev);
-    const float s32 = a.T <= 128 ? skinny_us<32, 2>(a, S32, 0.3f, 1.7f) : 1e30f;
-    const float s64 = skinny_us<64, 1>(a, S64, 0.335f, 3.2f), s64x2 = skinny_us<64, 2>(a, 1, 0.335f, 3.2f);
-    const float s128 = a.T > 64 ? skinny_us<128, 1>(a, S128, 0.39f, 6.8f) : 1e30f;
+    const float s32 = a.T <= 128 ? skinny_us<32, 2>(a, S32, 0.3f, 1.2f, 0.5f) : 1e30f;
+    const float s64 = skinny_us<64, 1>(a, S64, 0.335f, 1.8f, 1.4f);
+    const bool many = (long)((a.N + 127) / 128) * ((a.T + 63) / 64) > 148;
+    const float s64x2 = many ? skinny_us<64, 2>(a, 1, 0.265f, 2.2f, 0.f) : 1e30f;
+    const float s128 = a.T > 64 ? skinny_us<128, 1>(a, S128, 0.39f, 5.4f, 1.4f) : 1e30f;
     const float least = fminf(fminf(s32, s64), fminf(s64x2, s128));
     if (least < fminf(w128, w160))
       return least == s32     ? launch_skinny<32, 2>(a, dev, S32, st)
