@@ -10,6 +10,7 @@
 #include "mla_internal.cuh"
 #include "decode_tc.cuh"
 #include "proj_fp8.cuh"
+#include "proj_tc.cuh"
 #include "rows.cuh"
 
 namespace mla {
@@ -96,7 +97,7 @@ static void note_call(const void* stream, bool rows = false) {
   t_known = true;
   t_rows = rows;
 }
-static bool absorb_may_overlap(const void* stream) { return t_known && t_stream == stream && !t_rows; }
+bool absorb_may_overlap(const void* stream) { return t_known && t_stream == stream && !t_rows; }
 
 static mla_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
@@ -231,10 +232,10 @@ mla_status mla_absorb_query(const mla_dims* dims, const void* q_nope, const void
     return MLA_ERR_INVALID_ARG;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
-  const bool overlap = absorb_may_overlap(stream);
-  note_call(stream);
-  return cuda_status(launch_absorb(*dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin,
-                                   rope_rows, q_packed, err, overlap, static_cast<cudaStream_t>(stream)));
+  const cudaError_t e = launch_absorb(*dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin,
+                                      rope_rows, q_packed, err, static_cast<cudaStream_t>(stream));
+  note_call(stream);  // (after the launch, which asks what was in front)
+  return cuda_status(e);
 }
 
 size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t s_q,

@@ -85,7 +85,7 @@ size_t append_workspace_bytes(const mla_dims& d, int n_tok);
 
 cudaError_t launch_absorb(const mla_dims& d, const void* q_nope, const void* q_rope,
                           const int32_t* q_pos, int n_tok, const void* w_uk, const float* rcos,
-                          const float* rsin, int rope_rows, void* q_packed, int* err, bool overlap,
+                          const float* rsin, int rope_rows, void* q_packed, int* err,
                           cudaStream_t st);
 
 cudaError_t launch_output_up(const mla_dims& d, const void* o_lat, int n_tok, const void* w_uv,

@@ -13,7 +13,7 @@
 
 #include "mla_internal.cuh"
 #include "proj_fp8.cuh"
-#include "sm100_ptx.cuh"
+#include "sm100_f8.cuh"
 
 namespace mla {
 namespace p8 {

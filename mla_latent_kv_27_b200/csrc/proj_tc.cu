@@ -882,7 +882,7 @@ bool tc_absorb_fused_supported(const mla_dims& d) {
 
 cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* q_rope, const int32_t* q_pos,
                              int n_tok, const void* w_uk, const float* rcos, const float* rsin, int rope_rows,
-                             void* q_packed, int* err, bool overlap, cudaStream_t st) {
+                             void* q_packed, int* err, cudaStream_t st) {
   if (n_tok <= 0) return cudaSuccess;
   if ((n_tok + 63) / 64 > 65535) return kUnsupported;
   // 16-byte vector loads and stores of the RoPE part (callers check with absorb_tc_aligned)
@@ -922,7 +922,7 @@ cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() && overlap ? 1 : 0;  // (q_nope is read before the wait)
+  cfg.numAttrs = pdl_enabled() && absorb_may_overlap(st) ? 1 : 0;  // (q_nope is read before the wait)
   e = cudaLaunchKernelEx(&cfg, ptc::absorb_tc_kernel, mw, mq, mo, p);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

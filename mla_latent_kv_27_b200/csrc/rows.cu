@@ -10,7 +10,7 @@
 // fp32, nothing is rounded before it is stored.
 #include "mla_internal.cuh"
 #include "rows.cuh"
-#include "sm100_ptx.cuh"
+#include "sm100_f8.cuh"
 
 namespace mla {
 namespace rows {
