@@ -481,29 +481,135 @@ __global__ void __launch_bounds__(NT) rows_stream_kernel(const RowsArgs a, int s
 }
 
 // ------------------------------------------------------------------ norm / quantise, any layout
-// One CTA per row, element accesses: any width, alignment and leading dimension.  The row is
-// read twice (statistics, then outputs); a thread reads an element before it writes any output
-// of it, so sum_out and y may be the inputs' own memory.
-template <typename T, bool NORM>
-__global__ void __launch_bounds__(256) rows_any_kernel(const RowsArgs a) {
+// Element accesses: any width, alignment and leading dimension.  `units` warps share a row, each with J
+// blocks of 128 values in registers (lane l holds l, l + 32, l + 64, l + 96 of a block), so all loads
+// of a thread are in flight at once and the row is read once.  Where a norm's row takes more than one warp
+// they are a CTA; else, and without a norm, the warps are independent.  4000 x 7169 bf16 with the residual
+// and every output: 103 us (two passes over the row by 256 threads took 134), one such row 5.0 (15).
+// Every value is read before any output of it is written, so sum_out and y may be the inputs' own memory.
+template <typename T, bool NORM, int J>
+__global__ void __launch_bounds__(1024) rows_any_kernel(const RowsArgs a, int units) {
+  __shared__ float part[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const unsigned unit = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  const long row = unit / (unsigned)units;
+  if (row >= a.n_tok) return;  // (never a part of a row's warps)
+  const int b0 = (int)(unit % (unsigned)units), blocks = (a.width + 127) / 128;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
+  T in[J][4];
+  float v[J][4];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (b0 + j * units) * 128 + lane + 32 * i;
+      in[j][i] = k < a.width ? x[k] : from_f32<T>(0.f);
+    }
+  if (NORM && a.residual) {
+    const T* res = static_cast<const T*>(a.residual) + row * a.residual_ld;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = (b0 + j * units) * 128 + lane + 32 * i;
+        v[j][i] = k < a.width ? to_f32(res[k]) : 0.f;
+      }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] += to_f32(in[j][i]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = to_f32(in[j][i]);
+  }
+  const T* gamma = NORM ? static_cast<const T*>(a.gamma) : nullptr;
+  if (J <= 2 && gamma) {  // under way during the sum (more blocks leave no registers for it)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = (b0 + j * units) * 128 + lane + 32 * i;
+        in[j][i] = k < a.width ? gamma[k] : from_f32<T>(0.f);
+      }
+  }
+  float inv = 1.f;
+  if (NORM) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+    inv = __frsqrt_rn((units > 1 ? cta_sum(ss, part) : warp_sum(ss)) / (float)a.width + a.eps);
+  }
+  T* so = NORM && a.sum_out ? static_cast<T*>(a.sum_out) + row * a.sum_ld : nullptr;
+  T* y = NORM && a.y ? static_cast<T*>(a.y) + row * a.y_ld : nullptr;
+  uint8_t* q = a.codes ? a.codes + row * a.codes_ld : nullptr;
+  float m[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    m[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (b0 + j * units) * 128 + lane + 32 * i;
+      if (k < a.width) {
+        if (so) so[k] = from_f32<T>(v[j][i]);
+        if (NORM) v[j][i] = gamma ? v[j][i] * inv * to_f32(J <= 2 ? in[j][i] : gamma[k]) : v[j][i] * inv;
+        if (y) y[k] = from_f32<T>(v[j][i]);
+        m[j] = max_nan(m[j], fabsf(v[j][i]));
+      }
+    }
+  }
+  if (!q) return;
+  // maxima of the J blocks, block j's in the lanes with lane % J == j; each lane divides for its block
+#pragma unroll
+  for (int o = 1; o < J; o *= 2)
+#pragma unroll
+    for (int j = 0; j < J; j += 2 * o) {
+      const bool odd = (lane & o) != 0;
+      m[j] = max_nan(odd ? m[j + o] : m[j], __shfl_xor_sync(0xffffffffu, odd ? m[j] : m[j + o], o));
+    }
+#pragma unroll
+  for (int o = J; o < 32; o *= 2) m[0] = max_nan(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+  float ms, mi;
+  block_scale(m[0], ms, mi);
+  const int mine = b0 + lane * units;
+  if (lane < J && mine < blocks) a.scales[row * blocks + mine] = ms;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const float iv = __shfl_sync(0xffffffffu, mi, j);
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const int k = (b0 + j * units) * 128 + lane + 32 * i;
+      const uint32_t c = e4m3x2(__fmul_rn(v[j][i], iv), __fmul_rn(v[j][i + 1], iv));
+      if (k < a.width) q[k] = (uint8_t)c;
+      if (k + 32 < a.width) q[k + 32] = (uint8_t)(c >> 8);
+    }
+  }
+}
+
+// Norm of rows that neither this nor the vector kernels hold: one CTA per row, read twice (statistics,
+// then outputs).
+template <typename T>
+__global__ void __launch_bounds__(1024) rows_long_kernel(const RowsArgs a) {
   __shared__ float part[32];
   griddep_wait();
   griddep_launch_dependents();
   const long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
-  const T* res = NORM && a.residual ? static_cast<const T*>(a.residual) + row * a.residual_ld : nullptr;
-  const T* gamma = NORM ? static_cast<const T*>(a.gamma) : nullptr;
-  float inv = 1.f;
-  if (NORM) {
-    float ss = 0.f;
-    for (int i = threadIdx.x; i < a.width; i += blockDim.x) {
-      const float r = to_f32(x[i]) + (res ? to_f32(res[i]) : 0.f);
-      ss = fmaf(r, r, ss);
-    }
-    inv = __frsqrt_rn(cta_sum(ss, part) / (float)a.width + a.eps);
+  const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_ld : nullptr;
+  const T* gamma = static_cast<const T*>(a.gamma);
+  float ss = 0.f;
+  for (int i = threadIdx.x; i < a.width; i += blockDim.x) {
+    const float r = to_f32(x[i]) + (res ? to_f32(res[i]) : 0.f);
+    ss = fmaf(r, r, ss);
   }
-  T* so = NORM && a.sum_out ? static_cast<T*>(a.sum_out) + row * a.sum_ld : nullptr;
-  T* y = NORM && a.y ? static_cast<T*>(a.y) + row * a.y_ld : nullptr;
+  const float inv = __frsqrt_rn(cta_sum(ss, part) / (float)a.width + a.eps);
+  T* so = a.sum_out ? static_cast<T*>(a.sum_out) + row * a.sum_ld : nullptr;
+  T* y = a.y ? static_cast<T*>(a.y) + row * a.y_ld : nullptr;
   uint8_t* q = a.codes ? a.codes + row * a.codes_ld : nullptr;
   const int blocks = (a.width + 127) / 128;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -515,7 +621,7 @@ __global__ void __launch_bounds__(256) rows_any_kernel(const RowsArgs a) {
       v[i] = 0.f;
       if (k < a.width) {
         const float r = to_f32(x[k]) + (res ? to_f32(res[k]) : 0.f);
-        v[i] = NORM ? (gamma ? r * inv * to_f32(gamma[k]) : r * inv) : r;
+        v[i] = gamma ? r * inv * to_f32(gamma[k]) : r * inv;
         if (so) so[k] = from_f32<T>(r);
         if (y) y[k] = from_f32<T>(v[i]);
         m = max_nan(m, fabsf(v[i]));
@@ -801,8 +907,22 @@ template <typename T>
 static cudaError_t rows_impl(const RowsArgs& a, bool norm, cudaStream_t st) {
   using namespace rows;
   if (!rows_vector_ok<T>(a, norm)) {
-    return norm ? launch_pdl(rows_any_kernel<T, true>, (unsigned)a.n_tok, 256, st, 0, a)
-                : launch_pdl(rows_any_kernel<T, false>, (unsigned)a.n_tok, 256, st, 0, a);
+    // Blocks a warp: two for rows that come few at a time, else four (us on B200, two / four: norm 64 x 7001
+    // 5.3 / 6.9, 4000 x 7169 bf16 128 / 103; quantise 64 x 7001 1.8 / 2.0, 3000 x 9001 bf16 32 / 29), but two
+    // for the quantisation of floats (3000 x 9001 32 / 38).
+    const bool few = a.n_tok <= 592;
+    const int blocks = (a.width + 127) / 128;
+    if (norm && blocks > 4) {  // a row per CTA
+      if (blocks > 128) return launch_pdl(rows_long_kernel<T>, (unsigned)a.n_tok, 1024, st, 0, a);
+      const int n = few && blocks <= 64 ? 2 : 4, units = (blocks + n - 1) / n;
+      return launch_pdl(n == 2 ? rows_any_kernel<T, true, 2> : rows_any_kernel<T, true, 4>, (unsigned)a.n_tok, units * 32, st,
+                        0, a, units);
+    }
+    const int n = !norm && (few || sizeof(T) == 4) ? 2 : 4, units = (blocks + n - 1) / n;
+    const long ctas = ((long)units * a.n_tok + RW_WARPS - 1) / RW_WARPS;
+    if (ctas > 0x3fffffffl) return kUnsupported;  // (unit numbers are 32 bits)
+    auto kernel = norm ? rows_any_kernel<T, true, 4> : n == 2 ? rows_any_kernel<T, false, 2> : rows_any_kernel<T, false, 4>;
+    return launch_pdl(kernel, (unsigned)ctas, RW_WARPS * 32, st, 0, a, units);
   }
   const int chunks = a.width / 8;
   if (!norm) {

@@ -127,6 +127,27 @@ def test_norm_many_rows(lib, act, width, res, gamma, outs):
     run_norm(lib, act, 1201 if width <= 2056 else 641, width, res=res, gamma=gamma, outs=outs, pad=16, seed=width)
 
 
+# widths off the 8-value chunk: one and several warps a row, two and four blocks a warp, rows read twice
+@pytest.mark.parametrize("act", ACT)
+@pytest.mark.parametrize("t,width", [(3, 129), (700, 301), (701, 511), (4, 513), (601, 1501), (5, 8191), (2, 8193), (600, 7169),
+                                     (2, 16383), (3, 16385)])
+def test_norm_odd_widths(lib, act, t, width):
+    run_norm(lib, act, t, width, seed=width)
+    run_norm(lib, act, t, width, res=False, outs=("y",), seed=width)
+
+
+@pytest.mark.parametrize("act", ACT)
+@pytest.mark.parametrize("t,width", [(1, 1), (3, 255), (700, 257), (601, 1501), (2, 40001)])
+def test_quantize_odd_widths(lib, act, t, width):
+    x = randn((t, width), width).to(act)
+    q = torch.full((t, width + 3), 99, dtype=torch.uint8, device="cuda")
+    s = torch.full((t, -(-width // 128)), float("nan"), device="cuda")
+    lib.mla_quantize_rows(dt(lib, act), x, width, t, width, q, width + 3, s)
+    torch.cuda.synchronize()
+    check_codes(q, s, x.double(), width, 2.0 ** -24)
+    assert (q[:, width:] == 99).all()
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (1, 0), (0, 1), (24, 8)])
 def test_norm_strides_and_alignment(lib, pad, offset):
     for act in ACT:
