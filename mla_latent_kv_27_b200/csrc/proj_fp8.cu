@@ -796,12 +796,31 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
             bulk_commit_group();
           }
         } else {
+          // lanes along the outputs of a token, two of them each where every row is 4-byte aligned
           __syncwarp();
-          for (int e = lane; e < 32 * 16; e += 32) {
-            const int r = e / 16, c = e % 16, at = c * (int)sizeof(T);
-            if (row0 + r < p.T && cs + c < p.N)
-              static_cast<T*>(p.out)[(long)(row0 + r) * p.out_ld + cs + c] = *reinterpret_cast<const T*>(
-                  buf + r * ROW + (((at >> 4) ^ (sizeof(T) == 4 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4) + (at & 15));
+          const bool pairs = sizeof(T) == 2 && ((reinterpret_cast<uintptr_t>(p.out) >> 1 | p.out_ld) & 1) == 0;
+          const int wide = pairs ? 2 : 1, c = lane * wide % 16;
+          const int r0 = lane * wide / 16, left = p.T - row0 - r0, here = p.N - cs - c;
+          T* o = static_cast<T*>(p.out) + (long)(row0 + r0) * p.out_ld + cs + c;
+          auto staged = [&](int r) {
+            const int at = c * (int)sizeof(T);
+            return buf + r * ROW + (((at >> 4) ^ (sizeof(T) == 4 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4) + (at & 15);
+          };
+          if (pairs) {
+#pragma unroll
+            for (int r = 0; r < 32; r += 4, o += 4 * p.out_ld) {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(staged(r0 + r));
+              if (r < left && here > 1)
+                *reinterpret_cast<uint32_t*>(o) = v;
+              else if (r < left && here == 1)
+                *reinterpret_cast<uint16_t*>(o) = (uint16_t)v;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 32; r += 2, o += 2 * p.out_ld) {
+              const T v = *reinterpret_cast<const T*>(staged(r0 + r));
+              if (r < left && here > 0) *o = v;
+            }
           }
         }
       }
