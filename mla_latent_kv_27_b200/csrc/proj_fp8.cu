@@ -10,6 +10,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "mla_internal.cuh"
 #include "proj_fp8.cuh"
@@ -763,66 +764,86 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
       }
       if (!ok && lane == 0) record_error(p.err, ERR_TIMEOUT, 66);
       if (!ok) break;
-      // ---- the tile: 32 tokens x WN / 2 outputs of this warp, 16 outputs at a time
-      constexpr int ROW = 16 * sizeof(T), NBUF = 4096 / (32 * ROW);  // bytes of a staged row; buffers
+      // ---- the tile: 32 tokens x WN / 2 outputs of this warp
+      auto sixteen_bytes = [&](int c) {  // from sum c on, rounded
+        if constexpr (sizeof(T) == 4) {
+          return make_uint4(__float_as_uint(acc[c]), __float_as_uint(acc[c + 1]), __float_as_uint(acc[c + 2]),
+                            __float_as_uint(acc[c + 3]));
+        } else {
+          uint32_t h[4];
 #pragma unroll
-      for (int j = 0; j < C::HC / 16; ++j) {
-        uint8_t* buf = stg + (j % NBUF) * 32 * ROW;
-        if (TMA_OUT && lane == 0) bulk_wait_group_read<NBUF - 1>();  // the buffer's last store has read it
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < ROW / 16; ++q) {  // 16 bytes, at the place that the 64- or 32-byte swizzle gives them
-          uint4 w;
-          if constexpr (sizeof(T) == 4) {
-            w = make_uint4(__float_as_uint(acc[j * 16 + 4 * q]), __float_as_uint(acc[j * 16 + 4 * q + 1]),
-                           __float_as_uint(acc[j * 16 + 4 * q + 2]), __float_as_uint(acc[j * 16 + 4 * q + 3]));
-          } else {
-            uint32_t h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(acc[j * 16 + 8 * q + 2 * i], acc[j * 16 + 8 * q + 2 * i + 1]);
-              h[i] = *reinterpret_cast<const uint32_t*>(&x);
-            }
-            w = make_uint4(h[0], h[1], h[2], h[3]);
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c + 2 * i], acc[c + 2 * i + 1]);
+            h[i] = *reinterpret_cast<const uint32_t*>(&x);
           }
-          *reinterpret_cast<uint4*>(buf + lane * ROW + ((q ^ (sizeof(T) == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1)) << 4)) = w;
+          return make_uint4(h[0], h[1], h[2], h[3]);
         }
-        const int cs = n0 + half * C::HC + j * 16;
-        if (TMA_OUT) {
+      };
+      constexpr int PER16 = 16 / (int)sizeof(T);
+      if constexpr (TMA_OUT) {  // 16 outputs at a time
+        constexpr int ROW = 16 * sizeof(T), NBUF = 4096 / (32 * ROW);  // bytes of a staged row; buffers
+#pragma unroll
+        for (int j = 0; j < C::HC / 16; ++j) {
+          uint8_t* buf = stg + (j % NBUF) * 32 * ROW;
+          if (lane == 0) bulk_wait_group_read<NBUF - 1>();  // the buffer's last store has read it
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < ROW / 16; ++q)  // 16 bytes, at the place that the 64- or 32-byte swizzle gives them
+            *reinterpret_cast<uint4*>(buf + lane * ROW + ((q ^ (sizeof(T) == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1)) << 4)) =
+                sixteen_bytes(j * 16 + PER16 * q);
+          const int cs = n0 + half * C::HC + j * 16;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (row0 < p.T && cs < p.N) tma_store_2d(&tm_out, buf, cs, row0);  // clipped to T x N
             bulk_commit_group();
           }
-        } else {
-          // lanes along the outputs of a token, two of them each where every row is 4-byte aligned
+        }
+      } else {
+        // 128 bytes of each row at a time (what is left of WN / 2 at the end), stored with the lanes along the
+        // row: 4 bytes each where every row is 4-byte aligned, else a bf16 value each.  (Rows that straddle
+        // sectors cost two writes at each end of a segment: 4011 x 14142 x 176 to floats 88 us,
+        // 103 with segments of 16 outputs.)
+        const bool words = sizeof(T) == 4 || ((reinterpret_cast<uintptr_t>(p.out) >> 1 | p.out_ld) & 1) == 0;
+        auto segment = [&](auto count, int c0) {
+          constexpr int N = decltype(count)::value, BYTES = N * (int)sizeof(T);
           __syncwarp();
-          const bool pairs = sizeof(T) == 2 && ((reinterpret_cast<uintptr_t>(p.out) >> 1 | p.out_ld) & 1) == 0;
-          const int wide = pairs ? 2 : 1, c = lane * wide % 16;
-          const int r0 = lane * wide / 16, left = p.T - row0 - r0, here = p.N - cs - c;
-          T* o = static_cast<T*>(p.out) + (long)(row0 + r0) * p.out_ld + cs + c;
-          auto staged = [&](int r) {
-            const int at = c * (int)sizeof(T);
-            return buf + r * ROW + (((at >> 4) ^ (sizeof(T) == 4 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4) + (at & 15);
-          };
-          if (pairs) {
 #pragma unroll
-            for (int r = 0; r < 32; r += 4, o += 4 * p.out_ld) {
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(staged(r0 + r));
-              if (r < left && here > 1)
+          for (int q = 0; q < BYTES / 16; ++q)
+            *reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) = sixteen_bytes(c0 + PER16 * q);
+          __syncwarp();
+          auto staged = [&](int r, int at) { return stg + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15); };
+          const int cs = n0 + half * C::HC + c0;
+          if (words) {
+            constexpr int L = BYTES / 4, RP = 32 / L, V = 4 / (int)sizeof(T);  // lanes a row, rows at once, values a lane
+            const int u = lane % L, r0 = lane / L, left = p.T - row0 - r0, here = p.N - cs - u * V;
+            T* o = static_cast<T*>(p.out) + (long)(row0 + r0) * p.out_ld + cs + u * V;
+#pragma unroll 8
+            for (int r = 0; r < 32; r += RP, o += RP * p.out_ld) {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(staged(r0 + r, 4 * u));
+              if (r < left && here >= V)
                 *reinterpret_cast<uint32_t*>(o) = v;
-              else if (r < left && here == 1)
+              else if (r < left && here > 0)  // the first of two
                 *reinterpret_cast<uint16_t*>(o) = (uint16_t)v;
             }
-          } else {
+          } else if constexpr (sizeof(T) == 2) {
+            constexpr int L = N < 32 ? N : 32, RP = 32 / L;
 #pragma unroll
-            for (int r = 0; r < 32; r += 2, o += 2 * p.out_ld) {
-              const T v = *reinterpret_cast<const T*>(staged(r0 + r));
-              if (r < left && here > 0) *o = v;
+            for (int h = 0; h < N; h += L) {
+              const int c = h + lane % L, r0 = lane / L, left = p.T - row0 - r0, here = p.N - cs - c;
+              T* o = static_cast<T*>(p.out) + (long)(row0 + r0) * p.out_ld + cs + c;
+#pragma unroll 8
+              for (int r = 0; r < 32; r += RP, o += RP * p.out_ld) {
+                const T v = *reinterpret_cast<const T*>(staged(r0 + r, 2 * c));
+                if (r < left && here > 0) *o = v;
+              }
             }
           }
-        }
+        };
+        constexpr int FULL = 128 / (int)sizeof(T), REST = C::HC % FULL;
+#pragma unroll
+        for (int c0 = 0; c0 + FULL <= C::HC; c0 += FULL) segment(std::integral_constant<int, FULL>(), c0);
+        if constexpr (REST > 0) segment(std::integral_constant<int, REST>(), C::HC - REST);
       }
     }
     tmem_wait_ld();
@@ -1068,8 +1089,8 @@ static cudaError_t launch_narrow(const Fp8Args& a, int dev, cudaStream_t st) {
 //                                                          128x7168x16384: 33 (64 columns: 50)
 //   many tokens, 128 outputs  waves (0.26 blocks + 0.75) + 2.8           256x7168x16384: 38 (few-token: 58)
 //   many tokens, 160 outputs  waves (0.307 blocks + 2) + 2.8             2048x7168x16384: 233 (128 outputs: 290)
-// and 3.5 more a wave of the many-token kernel whose output rows TMA stores do not take
-// (333x1999x2000: 12.6, few-token 9).
+// and 1.5 more a wave of the many-token kernel whose output rows TMA stores do not take (333x1999x2000:
+// 11.0, few-token 8.8; 470x5329x256 7.3, few-token 8.3).
 template <int BN, int OCC>
 static float skinny_us(const Fp8Args& a, int S, float block, float wave, float exchange) {
   const int blocks = (a.K + 127) / 128;
@@ -1079,7 +1100,7 @@ static float skinny_us(const Fp8Args& a, int S, float block, float wave, float e
 }
 static float wide_us(const Fp8Args& a, int wn, float block, float wave) {
   const long tiles = (long)((a.N + wn - 1) / wn) * ((a.T + 255) / 256);
-  return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave + (out_aligned(a) ? 0.f : 3.5f)) + 2.8f;
+  return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave + (out_aligned(a) ? 0.f : 1.5f)) + 2.8f;
 }
 
 cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
