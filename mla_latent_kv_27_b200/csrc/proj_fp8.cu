@@ -995,9 +995,12 @@ static cudaError_t launch_fp8_any(const Fp8Args& a, cudaStream_t st) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Output tiles go out by TMA stores (boxes of 16 outputs x 32 rows) where its alignment rules allow.
+// Output tiles go out by TMA stores (boxes of 16 outputs x 32 rows) where its alignment rules allow, and where a row's
+// outputs end on 16 bytes: with 1087 bf16 outputs in rows of 1088 the clipped box was seen to write the last
+// element of the 4 bytes that it shares with an output.
 static bool out_aligned(const Fp8Args& a) {
-  return (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_ld * (a.act == MLA_F32 ? 4 : 2) % 16 == 0;
+  const int elt = a.act == MLA_F32 ? 4 : 2;
+  return (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_ld * elt % 16 == 0 && (int64_t)a.N * elt % 16 == 0;
 }
 static bool map_out(CUtensorMap* m, const Fp8Args& a) {
   auto enc = tmap_encoder();

@@ -118,10 +118,11 @@ def test_output_rows_apart(lib, out_pad):
 
 # many tokens and output rows that TMA stores do not take: 4-byte aligned or not, every end of a segment
 @pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("n", [1025, 1026, 1087, 1090, 1103, 1106, 1118, 1119])
+@pytest.mark.parametrize("n", [1025, 1026, 1028, 1032, 1087, 1090, 1103, 1106, 1118, 1119])
 def test_many_rows_odd_outputs(lib, act, n):
     run(lib, 2300, n, 144, act, seed=n)
     run(lib, 2049, n, 144, act, out_pad=1, seed=n)
+    run(lib, 2049, n, 144, act, out_pad=-n % 8 or 8, seed=n)  # aligned rows whose outputs end anywhere
 
 
 def test_zero_scale_and_zero_codes(lib):
