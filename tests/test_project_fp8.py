@@ -125,6 +125,21 @@ def test_many_rows_odd_outputs(lib, act, n):
     run(lib, 2049, n, 144, act, out_pad=-n % 8 or 8, seed=n)  # aligned rows whose outputs end anywhere
 
 
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t", [3, 50, 2100])
+@pytest.mark.parametrize("off", [1, 2, 8])
+def test_output_begins_anywhere(lib, act, t, off):
+    n, k = 1030, 256
+    x, w, xs, ws = codes((t, k), 1), codes((n, k), 2), scales((t, 2), 3), scales((9, 2), 4)
+    buf = torch.full((t * n + 16,), GUARD, dtype=act, device="cuda")
+    out = buf[off:off + t * n].view(t, n)
+    lib.mla_project_fp8(lib.MLA_BF16 if act == torch.bfloat16 else lib.MLA_F32, x, k, xs, t, w, ws, n, k, out, n)
+    torch.cuda.synchronize()
+    ref, absref = reference(x, xs, w, ws, t, n, k)
+    check(out, ref, absref, k)
+    assert (buf[:off] == GUARD).all() and (buf[off + t * n:] == GUARD).all()
+
+
 def test_zero_scale_and_zero_codes(lib):
     """A block of zero codes or a zero scale contributes exactly nothing, whatever is beside it."""
     t, n, k = 20, 130, 384
