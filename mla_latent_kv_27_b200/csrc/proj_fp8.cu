@@ -15,6 +15,7 @@
 #include "mla_internal.cuh"
 #include "proj_fp8.cuh"
 #include "sm100_f8.cuh"
+#include "store_ring.h"
 
 namespace mla {
 namespace p8 {
@@ -690,6 +691,9 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
     const float* my_scales = scales + quarter * 32 + lane;
     // all lanes' waits for a barrier
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_count(bar, parity)); };
+    // staged rows of 16 outputs, and buffers of 32 of them
+    constexpr int ROW = 16 * (int)sizeof(T), NBUF = 4096 / (32 * ROW);
+    StoreRing<NBUF> ring;  // (over all tiles: 160 outputs are 5 stores a tile, no multiple of NBUF)
     uint32_t cnt = 0, dph = 0;  // chunks of scales used; parity of the current use of accumulator d
     int d = 0;
     bool ok = true;
@@ -781,10 +785,9 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
       };
       constexpr int PER16 = 16 / (int)sizeof(T);
       if constexpr (TMA_OUT) {  // 16 outputs at a time
-        constexpr int ROW = 16 * sizeof(T), NBUF = 4096 / (32 * ROW);  // bytes of a staged row; buffers
 #pragma unroll
         for (int j = 0; j < C::HC / 16; ++j) {
-          uint8_t* buf = stg + (j % NBUF) * 32 * ROW;
+          uint8_t* buf = stg + ring.take() * 32 * ROW;
           if (lane == 0) bulk_wait_group_read<NBUF - 1>();  // the buffer's last store has read it
           __syncwarp();
 #pragma unroll

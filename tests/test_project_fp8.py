@@ -259,3 +259,13 @@ def test_chain_of_calls_without_a_wait_between(lib):
 
     a, b = run_chain(lambda: None), run_chain(torch.cuda.synchronize)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.isfinite(a[1]).all()
+
+
+# many tokens in tiles of 256 x 160 (by the choice's times: from some 11 scale blocks on, where 128 outputs take a
+# round of tiles more), 120 to 216 of them on 74 pairs, so that staging buffers, accumulators and scale slots go
+# on from one tile to the next; 9 token tiles are a group of 8 and a last one of one
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t,n,k", [(2304, 2560, 2048), (2304, 3840, 4096), (1300, 3200, 2560), (2300, 2552, 2000)])
+def test_many_tiles_of_160_outputs(lib, act, t, n, k):
+    run(lib, t, n, k, act, seed=21)
+    run(lib, t, n, k, act, out_pad=3, seed=22)
