@@ -23,6 +23,7 @@
  *     position outside the RoPE table) are not faults: the kernel skips the access and
  *     records the first such error in a per-device error word, read and cleared by
  *     mla_check_device_error().
+ *   - Any host thread may make a call, a thread that has made no CUDA call before among them.
  *   - The library caches, per device, the device addresses of its own static buffers (the
  *     error word, the no-allocation scratch).  Do not keep using it across a
  *     cudaDeviceReset (or anything else that destroys the device's primary context) in the

@@ -21,22 +21,22 @@ void note_launch(int n) { g_launches.fetch_add((unsigned long long)n, std::memor
 // Per-device error word (each device that loads the module gets its own copy).
 __device__ int g_error_word = 0;
 
-// The word's device address, looked up once per device (with that device current) and cached;
-// threads that race on a device's first call store the same address.  The cache assumes the
-// device's primary context lives as long as the process (no cudaDeviceReset in between).
+// The word's device address, looked up once per host thread and device (with that device current)
+// and cached.  Per thread, because the lookup is also what makes the device's context current to a
+// thread whose first CUDA call this is: the tensor maps are encoded by the driver, which asks for one.
+// The cache assumes the device's primary context lives as long as the process (no cudaDeviceReset in
+// between).
 static int* error_word_ptr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  static std::atomic<int*> ptrs[64];
+  static thread_local int* ptrs[64];
   if (dev < 0 || dev >= 64) return nullptr;
-  int* p = ptrs[dev].load(std::memory_order_acquire);
-  if (!p) {
+  if (!ptrs[dev]) {
     void* a = nullptr;
     if (cudaGetSymbolAddress(&a, g_error_word) != cudaSuccess || !a) return nullptr;
-    p = static_cast<int*>(a);
-    ptrs[dev].store(p, std::memory_order_release);
+    ptrs[dev] = static_cast<int*>(a);
   }
-  return p;
+  return ptrs[dev];
 }
 
 static bool dtype_ok(int t) { return t == MLA_F32 || t == MLA_BF16 || t == MLA_FP8_E4M3; }
