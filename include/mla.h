@@ -33,15 +33,13 @@
  *     MLA_F32 or MLA_BF16.  Accumulation is always fp32.
  *   - Overlap of consecutive calls (bf16 tensor-core path): the projection kernels of
  *     mla_append_cache, mla_absorb_query and mla_output_up are launched with programmatic
- *     stream serialization, and the preceding library kernel on the stream lets them start
- *     early.  Before waiting for that kernel to complete they read only their weights
- *     (w_dkv, w_kr, w_uk, w_uv), and q_nope in mla_absorb_query; everything else
- *     they read, and everything they write, comes after the wait.  So a weight (or query
- *     input) must not be an output of the immediately preceding library call on the same
- *     stream.  (Calls before that one have completed: a kernel lets the next one start only
- *     after its own wait.)  One exception: q_nope may come from mla_project_fp8 or mla_norm_rows
- *     directly in front, called by the same host thread; mla_absorb_query is then launched normally.
- *     Setting MLA_PDL=0 in the environment (read once) launches them all normally.
+ *     stream serialization, and the preceding kernel on the stream may let them start early (this
+ *     library's do).  Before waiting for that kernel to complete they read only their weights
+ *     (w_dkv, w_kr, w_uk, w_uv); everything else they read, and everything they write, comes
+ *     after the wait.  So a weight must not be an output of the kernel directly in front, this
+ *     library's or another's.  (The library's calls before that one have completed: each lets the
+ *     next one start only after its own wait.)  mla_absorb_query_early reads q_nope before the wait
+ *     too.  Setting MLA_PDL=0 in the environment (read once) launches them all normally.
  */
 #ifndef MLA_H_
 #define MLA_H_
@@ -153,6 +151,16 @@ MLA_API mla_status mla_absorb_query(const mla_dims* dims, const void* q_nope, co
                             const int32_t* q_pos, int32_t n_tok, const void* w_uk,
                             const float* rope_cos, const float* rope_sin, int32_t rope_rows,
                             void* q_packed, void* stream);
+
+/* mla_absorb_query_early — mla_absorb_query for a q_nope that is complete before the kernel directly
+ * in front starts.  The same arguments, checks and results; on the bf16 tensor-core path q_nope is
+ * read, and its products begun, while that kernel may still run.  The caller sees to it that directly
+ * in front of the call in its stream stands a call of this library that does not write q_nope
+ * (mla_append_cache, say), or nothing that may still be running. */
+MLA_API mla_status mla_absorb_query_early(const mla_dims* dims, const void* q_nope, const void* q_rope,
+                                  const int32_t* q_pos, int32_t n_tok, const void* w_uk,
+                                  const float* rope_cos, const float* rope_sin, int32_t rope_rows,
+                                  void* q_packed, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * mla_decode_attention — step 3 (+ step 4, the split combine): attention over the latent

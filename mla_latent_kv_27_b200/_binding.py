@@ -18,7 +18,7 @@ MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_DEVICE, 
 MLA_F32, MLA_BF16, MLA_FP8_E4M3 = 0, 1, 2
 
 EXPORTED = (
-    "mla_rope_table", "mla_append_workspace_size", "mla_append_cache", "mla_absorb_query",
+    "mla_rope_table", "mla_append_workspace_size", "mla_append_cache", "mla_absorb_query", "mla_absorb_query_early",
     "mla_decode_workspace_size", "mla_decode_attention", "mla_output_up", "mla_status_string",
     "mla_check_device_error", "mla_version", "mla_launch_count", "mla_decode_attention_noalloc",
     "mla_norm_rows", "mla_quantize_rows", "mla_project_fp8", "mla_append_rows",
@@ -59,6 +59,7 @@ def _load():
         "mla_append_workspace_size": (SZ, [D, I32]),
         "mla_append_cache": (I32, [D, P, I32, P, P, P, P, P, P, I32, C, P, SZ, P]),
         "mla_absorb_query": (I32, [D, P, P, P, I32, P, P, P, I32, P, P]),
+        "mla_absorb_query_early": (I32, [D, P, P, P, I32, P, P, P, I32, P, P]),
         "mla_decode_workspace_size": (SZ, [D, I32, I32, I32, I32]),
         "mla_decode_attention": (I32, [D, P, C, P, I32, I32, I32, I32, P, SZ, P, P, P]),
         "mla_output_up": (I32, [D, P, I32, P, P, P]),
@@ -179,6 +180,13 @@ def mla_absorb_query(dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_si
     _check(_lib.mla_absorb_query(ctypes.byref(dims), _p(q_nope), _p(q_rope), _p(q_pos), n_tok,
                                  _p(w_uk), _p(rope_cos), _p(rope_sin), rope_rows, _p(q_packed),
                                  _s(stream)), "mla_absorb_query")
+
+
+def mla_absorb_query_early(dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin, rope_rows,
+                           q_packed, stream=None):
+    _check(_lib.mla_absorb_query_early(ctypes.byref(dims), _p(q_nope), _p(q_rope), _p(q_pos), n_tok,
+                                       _p(w_uk), _p(rope_cos), _p(rope_sin), rope_rows, _p(q_packed),
+                                       _s(stream)), "mla_absorb_query_early")
 
 
 def mla_decode_workspace_size(dims, batch, s_q, n_split, max_pages_per_seq) -> int:

@@ -85,20 +85,6 @@ bool pdl_enabled() {
   return on;
 }
 
-// The calling thread's latest call that enqueued work: its stream, and whether its rows may be a q_nope
-// (the 8-bit projection's and the norm's may).  The absorb kernel reads q_nope before it waits for the
-// kernel in front of it, so it is launched without programmatic overlap unless that kernel is known to be a
-// call of this library that cannot have written q_nope.  (Only the kernel directly in front matters:
-// every kernel lets the next one start after its own wait, when all before it have completed.)
-static thread_local const void* t_stream = nullptr;
-static thread_local bool t_known = false, t_rows = false;
-static void note_call(const void* stream, bool rows = false) {
-  t_stream = stream;
-  t_known = true;
-  t_rows = rows;
-}
-bool absorb_may_overlap(const void* stream) { return t_known && t_stream == stream && !t_rows; }
-
 static mla_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
   if (e == kUnsupported) return MLA_ERR_UNSUPPORTED;
@@ -214,16 +200,15 @@ mla_status mla_append_cache(const mla_dims* dims, const void* h, int32_t n_tok,
   if (workspace_bytes < need || (need > 0 && !workspace)) return MLA_ERR_INVALID_ARG;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
-  note_call(stream);
   return cuda_status(launch_append(*dims, h, n_tok, seq_idx, pos, w_dkv, w_kr, rope_cos, rope_sin,
                                    rope_rows, make_view(dims, cache), static_cast<float*>(workspace),
                                    err, static_cast<cudaStream_t>(stream)));
 }
 
-mla_status mla_absorb_query(const mla_dims* dims, const void* q_nope, const void* q_rope,
-                            const int32_t* q_pos, int32_t n_tok, const void* w_uk,
-                            const float* rope_cos, const float* rope_sin, int32_t rope_rows,
-                            void* q_packed, void* stream) {
+static mla_status absorb_query(const mla_dims* dims, const void* q_nope, const void* q_rope,
+                               const int32_t* q_pos, int32_t n_tok, const void* w_uk,
+                               const float* rope_cos, const float* rope_sin, int32_t rope_rows,
+                               void* q_packed, bool q_early, void* stream) {
   mla_status s = check_dims(dims);
   if (s != MLA_OK) return s;
   if (n_tok < 0) return MLA_ERR_INVALID_ARG;
@@ -232,10 +217,25 @@ mla_status mla_absorb_query(const mla_dims* dims, const void* q_nope, const void
     return MLA_ERR_INVALID_ARG;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
-  const cudaError_t e = launch_absorb(*dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin,
-                                      rope_rows, q_packed, err, static_cast<cudaStream_t>(stream));
-  note_call(stream);  // (after the launch, which asks what was in front)
-  return cuda_status(e);
+  auto launch = q_early ? launch_absorb_early : launch_absorb;
+  return cuda_status(launch(*dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin, rope_rows,
+                            q_packed, err, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status mla_absorb_query(const mla_dims* dims, const void* q_nope, const void* q_rope,
+                            const int32_t* q_pos, int32_t n_tok, const void* w_uk,
+                            const float* rope_cos, const float* rope_sin, int32_t rope_rows,
+                            void* q_packed, void* stream) {
+  return absorb_query(dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin, rope_rows, q_packed,
+                      false, stream);
+}
+
+mla_status mla_absorb_query_early(const mla_dims* dims, const void* q_nope, const void* q_rope,
+                                  const int32_t* q_pos, int32_t n_tok, const void* w_uk,
+                                  const float* rope_cos, const float* rope_sin, int32_t rope_rows,
+                                  void* q_packed, void* stream) {
+  return absorb_query(dims, q_nope, q_rope, q_pos, n_tok, w_uk, rope_cos, rope_sin, rope_rows, q_packed,
+                      true, stream);
 }
 
 size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t s_q,
@@ -296,7 +296,6 @@ mla_status mla_decode_attention(const mla_dims* dims, const void* q_packed,
   a.o_lat = o_lat;
   a.lse = lse;
   a.err = err;
-  note_call(stream);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // the partitioned launchers run their own combine
   const DecodePath path = decode_path(dims);
@@ -317,7 +316,6 @@ mla_status mla_output_up(const mla_dims* dims, const void* o_lat, int32_t n_tok,
   if (!o_lat || !w_uv || !out) return MLA_ERR_INVALID_ARG;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
-  note_call(stream);
   return cuda_status(launch_output_up(*dims, o_lat, n_tok, w_uv, out, err, static_cast<cudaStream_t>(stream)));
 }
 
@@ -341,7 +339,6 @@ mla_status mla_norm_rows(int32_t act_dtype, const void* x, int64_t x_ld, const v
   if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, residual, residual_ld, gamma, n_tok, width, eps,
                       sum_out, sum_ld, y, y_ld, codes, codes_ld, scales, err};
-  note_call(stream, sum_out || y);
   return cuda_status(launch_rows(a, true, static_cast<cudaStream_t>(stream)));
 }
 
@@ -359,7 +356,6 @@ mla_status mla_quantize_rows(int32_t act_dtype, const void* x, int64_t x_ld, int
   if (!err) return MLA_ERR_CUDA;
   const RowsArgs a = {act_dtype, x, x_ld, nullptr, 0, nullptr, n_tok, width, 0.f,
                       nullptr, 0, nullptr, 0, codes, codes_ld, scales, err};
-  note_call(stream);
   return cuda_status(launch_rows(a, false, static_cast<cudaStream_t>(stream)));
 }
 
@@ -380,7 +376,6 @@ mla_status mla_project_fp8(int32_t act_dtype, const uint8_t* x_codes, int64_t x_
   if (!err) return MLA_ERR_CUDA;
   const Fp8Args a = {act_dtype, x_codes, x_ld, x_scales, w_codes, w_scales, n_tok, n_out, width,
                      out, out_ld, err};
-  note_call(stream, true);
   return cuda_status(launch_project_fp8(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -402,7 +397,6 @@ mla_status mla_append_rows(const mla_dims* dims, const void* kv, int64_t kv_ld, 
   if (n_tok > kMaxExtent || dims->d_c > kMaxExtent || dims->d_rope > kMaxExtent) return MLA_ERR_UNSUPPORTED;
   int* err = error_word_ptr();
   if (!err) return MLA_ERR_CUDA;
-  note_call(stream);
   return cuda_status(launch_append_rows(*dims, kv, kv_ld, n_tok, seq_idx, pos, gamma, eps, rope_cos,
                                         rope_sin, rope_rows, make_view(dims, cache), err,
                                         static_cast<cudaStream_t>(stream)));

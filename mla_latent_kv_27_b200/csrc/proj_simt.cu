@@ -279,11 +279,11 @@ __global__ void rope_query_kernel(const T* __restrict__ q_rope, const int32_t* _
 template <typename T>
 static cudaError_t absorb_impl(const mla_dims& d, const T* q_nope, const T* q_rope,
                                const int32_t* q_pos, int n_tok, const T* w_uk, const float* rcos,
-                               const float* rsin, int rope_rows, T* q_packed, int* err,
+                               const float* rsin, int rope_rows, T* q_packed, bool q_early, int* err,
                                cudaStream_t st) {
   const int H = d.n_heads, W = d.d_c + d.d_rope;
   if (sizeof(T) == 2 && tc_absorb_fused_supported(d) && absorb_tc_aligned(q_rope, q_packed, rcos, rsin))
-    return launch_absorb_tc(d, q_nope, q_rope, q_pos, n_tok, w_uk, rcos, rsin, rope_rows, q_packed, err, st);
+    return launch_absorb_tc(d, q_nope, q_rope, q_pos, n_tok, w_uk, rcos, rsin, rope_rows, q_packed, q_early, err, st);
   cudaError_t e;
   if (sizeof(T) == 2 && tc_proj_supported(d))
     e = launch_absorb_gemm_tc(d, q_nope, n_tok, w_uk, q_packed, err, st);
@@ -299,16 +299,30 @@ static cudaError_t absorb_impl(const mla_dims& d, const T* q_nope, const T* q_ro
   return cudaGetLastError();
 }
 
+static cudaError_t absorb_any(const mla_dims& d, const void* q_nope, const void* q_rope,
+                              const int32_t* q_pos, int n_tok, const void* w_uk, const float* rcos,
+                              const float* rsin, int rope_rows, void* q_packed, bool q_early, int* err,
+                              cudaStream_t st) {
+  if (d.act_dtype == MLA_F32)
+    return absorb_impl<float>(d, (const float*)q_nope, (const float*)q_rope, q_pos, n_tok,
+                              (const float*)w_uk, rcos, rsin, rope_rows, (float*)q_packed, q_early, err, st);
+  return absorb_impl<__nv_bfloat16>(d, (const __nv_bfloat16*)q_nope, (const __nv_bfloat16*)q_rope,
+                                    q_pos, n_tok, (const __nv_bfloat16*)w_uk, rcos, rsin,
+                                    rope_rows, (__nv_bfloat16*)q_packed, q_early, err, st);
+}
+
 cudaError_t launch_absorb(const mla_dims& d, const void* q_nope, const void* q_rope,
                           const int32_t* q_pos, int n_tok, const void* w_uk, const float* rcos,
                           const float* rsin, int rope_rows, void* q_packed, int* err,
                           cudaStream_t st) {
-  if (d.act_dtype == MLA_F32)
-    return absorb_impl<float>(d, (const float*)q_nope, (const float*)q_rope, q_pos, n_tok,
-                              (const float*)w_uk, rcos, rsin, rope_rows, (float*)q_packed, err, st);
-  return absorb_impl<__nv_bfloat16>(d, (const __nv_bfloat16*)q_nope, (const __nv_bfloat16*)q_rope,
-                                    q_pos, n_tok, (const __nv_bfloat16*)w_uk, rcos, rsin,
-                                    rope_rows, (__nv_bfloat16*)q_packed, err, st);
+  return absorb_any(d, q_nope, q_rope, q_pos, n_tok, w_uk, rcos, rsin, rope_rows, q_packed, false, err, st);
+}
+
+cudaError_t launch_absorb_early(const mla_dims& d, const void* q_nope, const void* q_rope,
+                                const int32_t* q_pos, int n_tok, const void* w_uk, const float* rcos,
+                                const float* rsin, int rope_rows, void* q_packed, int* err,
+                                cudaStream_t st) {
+  return absorb_any(d, q_nope, q_rope, q_pos, n_tok, w_uk, rcos, rsin, rope_rows, q_packed, true, err, st);
 }
 
 // ------------------------------------------------------------------ output up-projection

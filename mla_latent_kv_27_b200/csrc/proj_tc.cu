@@ -590,6 +590,7 @@ struct AbParams {
   const float* rcos;
   const float* rsin;
   int rope_rows;
+  int q_early;        // q_nope is read before the wait for the grid in front (which does not write it)
   __nv_bfloat16* q_packed;
   int* err;
 };
@@ -625,23 +626,36 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      // inputs only (weights, q_nope): no earlier grid of the stream writes them
-      mbar_arrive_expect_tx(&bars->bfull, (uint32_t)p.kchunks * 64 * BK * 2);
-      for (int kc = 0; kc < p.kchunks; ++kc)
-        tma_load_2d(smem + AB_B_OFF + kc * 64 * BK * 2, &tm_q, h * p.d_nope + kc * BK, n0, &bars->bfull);
-      int issued = 0;
-      for (int u = 0; u < units; ++u) {
+      // The weights may come before the grid in front has completed (no grid of the stream writes them), q_nope
+      // only where the caller says so (mla_absorb_query_early).
+      auto load_q = [&] {
+        mbar_arrive_expect_tx(&bars->bfull, (uint32_t)p.kchunks * 64 * BK * 2);
+        for (int kc = 0; kc < p.kchunks; ++kc)
+          tma_load_2d(smem + AB_B_OFF + kc * 64 * BK * 2, &tm_q, h * p.d_nope + kc * BK, n0, &bars->bfull);
+      };
+      auto load_w = [&](int u) {
         const int s = u % AB_NST;
-        if (u >= AB_NST && !mbar_wait(&bars->empty[s], ((u / AB_NST) - 1) & 1)) {
-          record_error(p.err, ERR_TIMEOUT, 50);
-          break;
-        }
         const int mb = u / p.kchunks, kc = u % p.kchunks;
         uint8_t* st = smem + s * A_BYTES;
         const int y = h * p.d_nope + kc * BK;
         mbar_arrive_expect_tx(&bars->full[s], A_BYTES);
         tma_load_2d(st, &tm_w, mb * 128, y, &bars->full[s]);
         tma_load_2d(st + A_BYTES / 2, &tm_w, mb * 128 + 64, y, &bars->full[s]);
+      };
+      if (p.q_early) load_q();
+      const int first = min(units, AB_NST);
+      for (int u = 0; u < first; ++u) load_w(u);
+      if (!p.q_early) {
+        griddep_wait();
+        load_q();
+      }
+      int issued = first;
+      for (int u = first; u < units; ++u) {
+        if (!mbar_wait(&bars->empty[u % AB_NST], ((u / AB_NST) - 1) & 1)) {
+          record_error(p.err, ERR_TIMEOUT, 50);
+          break;
+        }
+        load_w(u);
         issued = u + 1;
       }
       // no load of this CTA may still be in flight when it exits (bounded waits)
@@ -653,6 +667,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(128, 64, 1, 0);
+      if (!p.q_early) griddep_wait();  // (so that the wait for q_nope is not one for the grid in front)
       bool ok = mbar_wait(&bars->bfull, 0);
       if (!ok) record_error(p.err, ERR_TIMEOUT, 51);
       for (int u = 0; ok && u < units; ++u) {
@@ -882,7 +897,7 @@ bool tc_absorb_fused_supported(const mla_dims& d) {
 
 cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* q_rope, const int32_t* q_pos,
                              int n_tok, const void* w_uk, const float* rcos, const float* rsin, int rope_rows,
-                             void* q_packed, int* err, cudaStream_t st) {
+                             void* q_packed, bool q_early, int* err, cudaStream_t st) {
   if (n_tok <= 0) return cudaSuccess;
   if ((n_tok + 63) / 64 > 65535) return kUnsupported;
   // 16-byte vector loads and stores of the RoPE part (callers check with absorb_tc_aligned)
@@ -909,6 +924,7 @@ cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* 
   p.rcos = rcos;
   p.rsin = rsin;
   p.rope_rows = rope_rows;
+  p.q_early = q_early;
   p.q_packed = static_cast<__nv_bfloat16*>(q_packed);
   p.err = err;
   cudaError_t e = cudaFuncSetAttribute(ptc::absorb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ptc::AB_SMEM);
@@ -922,7 +938,7 @@ cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() && absorb_may_overlap(st) ? 1 : 0;  // (q_nope is read before the wait)
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, ptc::absorb_tc_kernel, mw, mq, mo, p);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

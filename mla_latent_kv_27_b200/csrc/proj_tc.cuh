@@ -9,11 +9,15 @@ bool tc_proj_supported(const mla_dims& d);
 // (W_UK[h]^T q_nope[t, h] || RoPE(q_rope[t, h])), bf16.  Shapes: tc_absorb_fused_supported.
 bool tc_absorb_fused_supported(const mla_dims& d);
 bool absorb_tc_aligned(const void* q_rope, const void* q_packed, const float* rcos, const float* rsin);
-// Whether the absorb may start under the kernel in front of it in the stream (api.cu).
-bool absorb_may_overlap(const void* stream);
+// q_early: q_nope is read while the kernel in front of this one in the stream may still run (right only where that
+// one is a kernel of this library that does not write q_nope).
 cudaError_t launch_absorb_tc(const mla_dims& d, const void* q_nope, const void* q_rope, const int32_t* q_pos,
                              int n_tok, const void* w_uk, const float* rcos, const float* rsin, int rope_rows,
-                             void* q_packed, int* err, cudaStream_t st);
+                             void* q_packed, bool q_early, int* err, cudaStream_t st);
+// launch_absorb with q_early (which only the kernel of launch_absorb_tc makes use of).
+cudaError_t launch_absorb_early(const mla_dims& d, const void* q_nope, const void* q_rope, const int32_t* q_pos,
+                                int n_tok, const void* w_uk, const float* rcos, const float* rsin, int rope_rows,
+                                void* q_packed, int* err, cudaStream_t st);
 // q_packed[t, h, 0:d_c] = W_UK[h]^T q_nope[t, h]  (bf16)
 cudaError_t launch_absorb_gemm_tc(const mla_dims& d, const void* q_nope, int n_tok, const void* w_uk,
                                   void* q_packed, int* err, cudaStream_t st);

@@ -180,10 +180,12 @@ class MLARunner:
                            self.w_kr, self.rope_cos, self.rope_sin, self.rope_rows, self.cache.desc,
                            self.append_ws, self.append_ws_bytes, stream or self.stream)
 
-    def absorb(self, stream=None):
-        B.mla_absorb_query(self.dims, self.q_nope, self.q_rope, self.pos, self.n_tok, self.w_uk,
-                           self.rope_cos, self.rope_sin, self.rope_rows, self.q_packed,
-                           stream or self.stream)
+    def absorb(self, stream=None, q_early=False):
+        """``q_early``: a library call that does not write q_nope stands directly in front
+        (mla_absorb_query_early)."""
+        absorb = B.mla_absorb_query_early if q_early else B.mla_absorb_query
+        absorb(self.dims, self.q_nope, self.q_rope, self.pos, self.n_tok, self.w_uk, self.rope_cos,
+               self.rope_sin, self.rope_rows, self.q_packed, stream or self.stream)
 
     def decode(self, stream=None):
         B.mla_decode_attention(self.dims, self.q_packed, self.cache.desc, self.seq_lens, self.batch,
@@ -196,7 +198,7 @@ class MLARunner:
 
     def step(self, stream=None):
         self.append(stream)
-        self.absorb(stream)
+        self.absorb(stream, q_early=True)  # (behind the append)
         self.decode(stream)
         self.output(stream)
         return self.out
@@ -275,8 +277,8 @@ class MLARunner:
             B.mla_append_cache(self.dims, h, self.n_tok, self.seq_idx, self.pos, self.w_dkv, self.w_kr,
                                self.rope_cos, self.rope_sin, self.rope_rows, self.cache.desc,
                                self.append_ws, self.append_ws_bytes, compute)
-            B.mla_absorb_query(self.dims, qn, qr, self.pos, self.n_tok, self.w_uk, self.rope_cos,
-                               self.rope_sin, self.rope_rows, self.q_packed, compute)
+            B.mla_absorb_query_early(self.dims, qn, qr, self.pos, self.n_tok, self.w_uk, self.rope_cos,
+                                     self.rope_sin, self.rope_rows, self.q_packed, compute)
             # -- the one boundary with event operations --
             consumed[k].record(compute)
             used[k] = True
@@ -369,10 +371,10 @@ class MLALayer(MLARunner):
                           self.q_nope, w.n_heads * w.d_nope, st)
         B.mla_project_fp8(self.act, self.q8, R, self.q8_s, T, self.w_qr, self.s_qr, w.n_heads * w.d_rope, R,
                           self.q_rope, w.n_heads * w.d_rope, st)
-        # (here, so that the absorb, which reads q_nope early, may start under it)
+        # (here, so that the absorb may read q_nope under it)
         B.mla_append_rows(self.dims, self.down[:, R:], self.d_down, T, self.seq_idx, self.pos, self.g_kv, self.eps,
                           self.rope_cos, self.rope_sin, self.rope_rows, self.cache.desc, st)
-        self.absorb(st)
+        self.absorb(st, q_early=True)
         self.decode(st)
         self.output(st)
         B.mla_quantize_rows(self.act, self.out, HV, T, HV, self.o8, HV, self.o8_s, st)
