@@ -32,7 +32,6 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
   __shared__ float xs_s[16][64 + 4];
   __shared__ float ws_s[16][64 + 4];
   griddep_wait();
-  griddep_launch_dependents();
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const long t0 = (long)blockIdx.y * 64;
   const int n0 = blockIdx.x * 64;
@@ -73,6 +72,9 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
       for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(part[i][j], s, acc[i][j]);
     }
   }
+  // (not before: the loop takes as long as the width says, and a grid that starts under it would count its bounded
+  // waits from its own start)
+  griddep_launch_dependents();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const long t = t0 + ty + 16 * i;
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
   tc_fence_after();
   if (S > 1) cluster_arrive();  // peers may send to this CTA after this
   const uint32_t tmem = bars->tmem_base;
+  griddep_wait();  // (every warp: none of the bounded waits below is for the grid in front)
 
   // sums of this thread's lane (output n0 + 32 quarter + lane) for its CW columns, as pairs
   uint64_t acc[C::CW / 2];
@@ -241,7 +244,6 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
   // (a wait for the phase before a barrier's first one returns at once)
   if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
-    griddep_wait();
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < nb; ++i) {
@@ -304,7 +306,6 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
   } else if (warp < 2 + C::SW) {
     // -------------------------------------------------------------- scales of the CTA's tokens
     // Eight lanes read the 32 bytes of a token's chunk.  Past the last token: zero.
-    griddep_wait();
     const float* ws = p.ws + (long)blockIdx.y * p.blocks;
     for (int c = 0; c * C::XC < nb; ++c) {
       if (!warp_wait(&bars->sempty[c & 1], ((c >> 1) & 1) ^ 1)) {
@@ -333,7 +334,6 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------------- promoting warps
-    griddep_wait();
     if (threadIdx.x == 128) griddep_launch_dependents();
     const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + col0;
     int s = 0;
@@ -551,6 +551,7 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
   cluster_wait();  // both CTAs' barriers are ready before either signals the other's
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  griddep_wait();  // (every warp: none of the bounded waits below is for the grid in front)
 
   // (a wait for the phase before a barrier's first one returns at once)
   if (warp < 4) {
@@ -560,7 +561,6 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
     // time, twice what the tensor pipe needs for them.
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer (both CTAs)
-      griddep_wait();
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -643,7 +643,6 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
       // xs[t, b] ws[r, b] for the two block rows r that a tile's outputs can meet.  Eight lanes read the 32 bytes of a
       // token's chunk.  Tokens and outputs past the ends take the last one's: what they give is not
       // stored.
-      griddep_wait();
       const int k = lane % C::XC, r0 = (warp - 2) * 64 + lane / C::XC;
       uint32_t cnt = 0;
       bool ok = true;
@@ -683,7 +682,6 @@ __global__ void __launch_bounds__(WdCfg<WN>::THREADS, 1)
   } else {
     // -------------------------------------------------------------- promoting warps
     setmaxnreg_inc<C::REGS_MANY>();
-    griddep_wait();
     if (threadIdx.x == 128) griddep_launch_dependents();
     const int quarter = warp & 3, half = (warp - 4) / 4;
     const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::HC;

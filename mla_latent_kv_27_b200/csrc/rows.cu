@@ -592,12 +592,12 @@ __global__ void __launch_bounds__(1024) rows_any_kernel(const RowsArgs a, int un
 }
 
 // Norm of rows that neither this nor the vector kernels hold: one CTA per row, read twice (statistics,
-// then outputs).
+// then outputs).  Its loops take as long as the width says, so it does not let the next grid start early (which would
+// count its bounded waits from its own start).
 template <typename T>
 __global__ void __launch_bounds__(1024) rows_long_kernel(const RowsArgs a) {
   __shared__ float part[32];
   griddep_wait();
-  griddep_launch_dependents();
   const long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_ld : nullptr;
@@ -803,11 +803,10 @@ __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const Append
 }
 
 // Any d_c, d_rope, alignment and leading dimension: one warp per token, element accesses, the
-// latent part read twice when it is normed.
+// latent part read twice when it is normed.  (No early start of the next grid, as in rows_long_kernel.)
 template <typename T, bool FP8>
 __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_any_kernel(const AppendParams p) {
   griddep_wait();
-  griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
   const long t = (long)blockIdx.x * AR_WARPS + threadIdx.x / 32;
   if (t >= p.T) return;

@@ -269,3 +269,42 @@ def test_chain_of_calls_without_a_wait_between(lib):
 def test_many_tiles_of_160_outputs(lib, act, t, n, k):
     run(lib, t, n, k, act, seed=21)
     run(lib, t, n, k, act, out_pad=3, seed=22)
+
+
+@pytest.mark.parametrize("follower", ["few", "split", "many", "core"])
+def test_behind_a_call_of_seconds(lib, follower):
+    """One output of 60 million values on the general kernel takes longer than a kernel's own bounded waits (2 s); the call
+    behind it does not count them from before that one's end, and nothing is reported."""
+    from mla_latent_kv_27_b200 import workloads as wl
+    k0 = 60_000_001
+    x0, w0 = codes((1, k0), 1), codes((1, k0), 2)
+    xs0, ws0 = scales((1, -(-k0 // 128)), 3) / 2 ** 10, scales((1, -(-k0 // 128)), 4) / 2 ** 10
+    long_out = torch.empty((1, 1), device="cuda")
+    if follower == "core":
+        from mla_latent_kv_27_b200.runner import MLARunner
+        r = MLARunner(wl.WORKLOADS["v2lite_bf16"], lengths=(130, 64))
+        r.draw_step_inputs()
+        call, outs = r.step, lambda: [r.cache.rows, r.q_packed, r.out]
+    else:
+        t, n, k = {"few": (5, 18810, 272), "split": (1, 576, 2048), "many": (300, 1000, 512)}[follower]
+        x, w, xs, ws = codes((t, k), 5), codes((n, k), 6), scales((t, -(-k // 128)), 7), scales((-(-n // 128), -(-k // 128)), 8)
+        out = torch.empty((t, n), device="cuda")
+        call = lambda: lib.mla_project_fp8(lib.MLA_F32, x, k, xs, t, w, ws, n, k, out, n)  # noqa: E731
+        outs = lambda: [out]  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs()]
+    for o in outs():
+        o.zero_()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    lib.mla_project_fp8(lib.MLA_F32, x0, k0, xs0, 1, w0, ws0, 1, k0, long_out, 1)
+    call()
+    b.record()
+    torch.cuda.synchronize()
+    assert a.elapsed_time(b) > 2500
+    assert lib.mla_check_device_error()[0] == 0
+    assert all(torch.equal(o, v) for o, v in zip(outs(), want))
+    s = (xs0 * ws0).double().repeat_interleave(128, 1)[:, :k0]
+    p = x0.view(torch.float8_e4m3fn).double() * w0.view(torch.float8_e4m3fn).double() * s
+    assert abs(float(long_out) - float(p.sum())) <= (256 + -(-k0 // 128) + 4) * 2.0 ** -24 * float(p.abs().sum())
