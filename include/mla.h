@@ -260,6 +260,7 @@ MLA_API mla_status mla_decode_attention_noalloc(const mla_dims* dims, const void
  *   - *_ld is the distance between consecutive rows in elements (bytes for codes), at least the
  *     row's width; elements between the width and *_ld are neither read nor written.
  *   - act_dtype is the element type of the unquantised rows: MLA_F32 or MLA_BF16.
+ *   - Rows, widths and outputs are counted up to 2^31 - 4097 each (more is MLA_ERR_UNSUPPORTED).
  *   - Any width and *_ld is taken, and any alignment of the elements' own size (less is
  *     MLA_ERR_INVALID_ARG).  16-byte aligned rows (8-byte codes) whose width is a multiple of 8
  *     take the faster, vectorised kernels.

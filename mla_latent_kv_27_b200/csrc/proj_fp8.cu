@@ -33,8 +33,9 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
   __shared__ float ws_s[16][64 + 4];
   griddep_wait();
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  const long t0 = (long)blockIdx.y * 64;
-  const int n0 = blockIdx.x * 64;
+  const unsigned tiles_n = (unsigned)(a.N + 63) / 64;
+  const long t0 = (long)(blockIdx.x / tiles_n) * 64;
+  const int n0 = (int)(blockIdx.x % tiles_n) * 64;
   const int blocks = (a.K + 127) / 128;
   float acc[4][4] = {};
   for (int b = 0; b < blocks; ++b) {
@@ -946,7 +947,6 @@ static cudaError_t launch_skinny(const Fp8Args& a, int dev, int S, cudaStream_t 
   if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN)) return kUnsupported;
   const int blocks = (a.K + 127) / 128, tiles_n = (a.N + 127) / 128;
   const long tiles_t = (a.T + BN - 1) / BN;
-  if (tiles_t > 65535 || tiles_n > 65535) return kUnsupported;
   p8::SkParams p;
   p.xs = a.xs;
   p.ws = a.ws;
@@ -980,9 +980,10 @@ static cudaError_t launch_skinny(const Fp8Args& a, int dev, int S, cudaStream_t 
 }
 
 static cudaError_t launch_fp8_any(const Fp8Args& a, cudaStream_t st) {
-  if ((a.T + 63) / 64 > 65535) return kUnsupported;
+  const long tiles = (long)((a.N + 63) / 64) * ((a.T + 63) / 64);
+  if (tiles > 0x7fffffffl) return kUnsupported;  // (17 TB of outputs)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + 63) / 64), (unsigned)((a.T + 63) / 64));
+  cfg.gridDim = dim3((unsigned)tiles);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1107,15 +1108,16 @@ static float wide_us(const Fp8Args& a, int wn, float block, float wave) {
   return (tiles + 73) / 74 * (block * ((a.K + 127) / 128) + wave + (out_aligned(a) ? 0.f : 1.5f)) + 2.8f;
 }
 
-cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
-  if (!tma_layout(a)) return launch_fp8_any(a, st);
+static cudaError_t launch_tensor_core(const Fp8Args& a, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (a.T <= 16) return launch_narrow<16>(a, dev, st);
-  if (a.T <= 32) return launch_narrow<32>(a, dev, st);
+  // the few-token kernels number their tiles of 128 outputs along a grid's y
+  const bool few = (a.N + 127) / 128 <= 65535;
+  if (a.T <= 16 && few) return launch_narrow<16>(a, dev, st);
+  if (a.T <= 32 && few) return launch_narrow<32>(a, dev, st);
   const float w128 = wide_us(a, 128, 0.26f, 0.75f), w160 = wide_us(a, 160, 0.307f, 2.f);
-  if (a.T <= 1024) {
+  if (a.T <= 1024 && few) {
     const int S32 = skinny_split<32, 2>(a, dev), S64 = skinny_split<64, 1>(a, dev), S128 = skinny_split<128, 1>(a, dev);
     const float s32 = a.T <= 128 ? skinny_us<32, 2>(a, S32, 0.3f, 1.2f, 0.5f) : 1e30f;
     const float s64 = skinny_us<64, 1>(a, S64, 0.335f, 1.8f, 1.4f);
@@ -1130,6 +1132,12 @@ cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
                               : launch_skinny<128, 1>(a, dev, S128, st);
   }
   return w128 < w160 ? launch_wide<128>(a, st) : launch_wide<160>(a, st);
+}
+
+cudaError_t launch_project_fp8(const Fp8Args& a, cudaStream_t st) {
+  // What no tensor map takes (a row distance of 2^40 bytes, say) goes to the general kernel as well.
+  const cudaError_t e = tma_layout(a) ? launch_tensor_core(a, st) : kUnsupported;
+  return e == kUnsupported ? launch_fp8_any(a, st) : e;
 }
 
 }  // namespace mla

@@ -308,3 +308,22 @@ def test_behind_a_call_of_seconds(lib, follower):
     s = (xs0 * ws0).double().repeat_interleave(128, 1)[:, :k0]
     p = x0.view(torch.float8_e4m3fn).double() * w0.view(torch.float8_e4m3fn).double() * s
     assert abs(float(long_out) - float(p.sum())) <= (256 + -(-k0 // 128) + 4) * 2.0 ** -24 * float(p.abs().sum())
+
+
+@pytest.mark.parametrize("t,n,k", [(2, 65535 * 128 + 130, 16), (40, 65535 * 128 + 130, 16), (65535 * 64 + 70, 3, 5),
+                                   (3, 65535 * 64 + 70, 5)])
+def test_more_tiles_than_a_grids_second_dimension(lib, t, n, k):
+    run(lib, t, n, k, torch.bfloat16, seed=31)
+
+
+def test_row_distance_past_a_tensor_maps(lib):
+    """One row may be any distance from the next, which there is none of; other calls take such rows elsewhere."""
+    n, k = 200, 512
+    x, w, xs, ws = codes((1, k), 1), codes((n, k), 2), scales((1, 4), 3), scales((2, 4), 4)
+    out = torch.full((1, n), GUARD, device="cuda")
+    for ld in (2 ** 40, 2 ** 41 + 16, 2 ** 62):
+        lib.mla_project_fp8(lib.MLA_F32, x, ld, xs, 1, w, ws, n, k, out, ld)
+        torch.cuda.synchronize()
+        check(out, *reference(x, xs, w, ws, 1, n, k), k)
+        out.fill_(GUARD)
+    assert lib.mla_check_device_error()[0] == 0
