@@ -302,12 +302,14 @@ BLOCK = 128  # values that share a scale
 
 def quantize_weight(w: torch.Tensor):
     """8-bit form of a weight [n, k]: E4M3 codes (uint8 [n, k]) and one fp32 scale per 128 x 128 block,
-    amax / 448 (1 for an all-zero block), as mla_project_fp8 takes them.  Done once per weight."""
+    amax / 448 (1 for an all-zero block), as mla_project_fp8 takes them.  A block whose amax is below 2^-100 is
+    coded against 2^-100 and one that holds a NaN or an infinity stands for NaN, as in the library's 8-bit
+    rows.  Done once per weight."""
     n, k = w.shape
     nb, kb = -(-n // BLOCK), -(-k // BLOCK)
     blocks = torch.nn.functional.pad(w.float(), (0, kb * BLOCK - k, 0, nb * BLOCK - n)).view(nb, BLOCK, kb, BLOCK)
     amax = blocks.abs().amax((1, 3))
-    scales = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))
+    scales = torch.where(amax == 0, torch.ones_like(amax), amax.clamp(min=2.0 ** -100) / E4M3_MAX)
     codes = (blocks / scales[:, None, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     codes = codes.view(nb * BLOCK, kb * BLOCK)[:n, :k].contiguous().view(torch.uint8)
     return codes, scales.contiguous()

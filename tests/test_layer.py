@@ -185,3 +185,26 @@ def test_absorb_directly_behind_the_norm(lib):
     L.q_packed.zero_()
     for _ in range(6):
         assert torch.equal(norm_and_absorb(lambda: None), want)
+
+
+def test_quantize_weight_of_tiny_and_not_finite_blocks():
+    """On the CPU: blocks of subnormals stay finite, and a NaN or an infinity makes its block NaN without touching the
+    blocks beside it (a scale of 1 would round its neighbours to multiples of 2^-9 and say nothing)."""
+    from mla_latent_kv_27_b200.runner import quantize_weight
+    g = torch.Generator().manual_seed(4)
+    w = torch.randn((256, 640), generator=g) / 40
+    w[:128, 128:256] *= 2.0 ** -140
+    w[3, 130] = 0
+    w[5, 260] = float("nan")
+    w[6, 390] = float("inf")
+    w[7, 520] = -float("inf")
+    codes, scales = quantize_weight(w)
+    s = scales.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+    v = codes.view(torch.float8_e4m3fn).double() * s
+    for b in (2, 3, 4):
+        assert torch.isnan(v[:128, 128 * b:128 * b + 128]).all()
+    good = torch.ones((256, 640), dtype=torch.bool)
+    good[:128, 256:] = False
+    err = (v - w.double()).abs()
+    # half a step of the code (2^-10 scales where it is subnormal), and the division's rounding
+    assert (err <= (2.0 ** -4 + 2.0 ** -20) * w.double().abs() + 2.0 ** -10 * s)[good].all()
