@@ -175,26 +175,30 @@ class MLARunner:
             t.copy_(torch.randn(t.shape, generator=gen, device=self.device, dtype=torch.float32))
 
     # ------------------------------------------------------------------ the step
+    def _on(self, stream):
+        """The stream of a call: the one given (0 is the legacy default stream), else the runner's."""
+        return self.stream if stream is None else stream
+
     def append(self, stream=None):
         B.mla_append_cache(self.dims, self.h_new, self.n_tok, self.seq_idx, self.pos, self.w_dkv,
                            self.w_kr, self.rope_cos, self.rope_sin, self.rope_rows, self.cache.desc,
-                           self.append_ws, self.append_ws_bytes, stream or self.stream)
+                           self.append_ws, self.append_ws_bytes, self._on(stream))
 
     def absorb(self, stream=None, q_early=False):
         """``q_early``: a library call that does not write q_nope stands directly in front
         (mla_absorb_query_early)."""
         absorb = B.mla_absorb_query_early if q_early else B.mla_absorb_query
         absorb(self.dims, self.q_nope, self.q_rope, self.pos, self.n_tok, self.w_uk, self.rope_cos,
-               self.rope_sin, self.rope_rows, self.q_packed, stream or self.stream)
+               self.rope_sin, self.rope_rows, self.q_packed, self._on(stream))
 
     def decode(self, stream=None):
         B.mla_decode_attention(self.dims, self.q_packed, self.cache.desc, self.seq_lens, self.batch,
                                self.w.s_q, int(self.w.causal or self.w.s_q > 1), self.n_split,
                                self.decode_ws, self.decode_ws_bytes, self.o_lat, self.lse,
-                               stream or self.stream)
+                               self._on(stream))
 
     def output(self, stream=None):
-        B.mla_output_up(self.dims, self.o_lat, self.n_tok, self.w_uv, self.out, stream or self.stream)
+        B.mla_output_up(self.dims, self.o_lat, self.n_tok, self.w_uv, self.out, self._on(stream))
 
     def step(self, stream=None):
         self.append(stream)
@@ -361,7 +365,7 @@ class MLALayer(MLARunner):
         self.y = torch.empty((T, w.d_model), dtype=dt, device=dev)
 
     def layer_step(self, stream=None):
-        w, T, st = self.w, self.n_tok, stream or self.stream
+        w, T, st = self.w, self.n_tok, self._on(stream)
         D, R, HV = w.d_model, self.q_rank, w.n_heads * w.d_v
         B.mla_norm_rows(self.act, self.h_new, D, self.residual, D, self.g_in, T, D, self.eps, self.residual, D,
                         None, 0, self.x8, D, self.x8_s, st)
