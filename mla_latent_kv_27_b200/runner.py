@@ -17,6 +17,8 @@ tokens at positions L_b - S_q .. L_b - 1, whose queries attend causally when S_q
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -135,6 +137,20 @@ class MLARunner:
         self.decode_ws_bytes = B.mla_decode_workspace_size(self.dims, self.batch, w.s_q, self.n_split,
                                                            int(table.shape[1]))
         self.decode_ws = torch.empty(max(1, self.decode_ws_bytes), dtype=torch.uint8, device=dev)
+        torch.cuda.synchronize(dev)  # what the current stream wrote here is there for any stream's step
+
+    @contextlib.contextmanager
+    def _on_own_stream(self):
+        """The body's torch operations go to the runner's stream, with the library's calls, behind what the
+        current stream was given before and in front of what it is given after."""
+        cur = torch.cuda.current_stream(self.device)
+        own = cur if self.stream is None else self.stream
+        if isinstance(own, int):
+            own = torch.cuda.ExternalStream(own, self.device)
+        own.wait_stream(cur)
+        with torch.cuda.stream(own):
+            yield
+        cur.wait_stream(own)
 
     # ------------------------------------------------------------------ cache contents
     def fill_cache_projected(self, chunk: int = 16384, seed: int = 0):
@@ -149,14 +165,15 @@ class MLARunner:
         total = len(seq)
         dt = _TORCH[w.act_dtype]
         ws_bytes = B.mla_append_workspace_size(self.dims, min(chunk, max(total, 1)))
-        ws = torch.empty(max(1, ws_bytes), dtype=torch.uint8, device=self.device)
-        for lo in range(0, total, chunk):
-            hi = min(total, lo + chunk)
-            h = torch.randn((hi - lo, w.d_model), generator=gen, device=self.device, dtype=torch.float32).to(dt)
-            s_t = torch.as_tensor(seq[lo:hi], device=self.device)
-            p_t = torch.as_tensor(pos[lo:hi], device=self.device)
-            B.mla_append_cache(self.dims, h, hi - lo, s_t, p_t, self.w_dkv, self.w_kr, self.rope_cos,
-                               self.rope_sin, self.rope_rows, self.cache.desc, ws, ws_bytes, self.stream)
+        with self._on_own_stream():
+            ws = torch.empty(max(1, ws_bytes), dtype=torch.uint8, device=self.device)
+            for lo in range(0, total, chunk):
+                hi = min(total, lo + chunk)
+                h = torch.randn((hi - lo, w.d_model), generator=gen, device=self.device, dtype=torch.float32).to(dt)
+                s_t = torch.as_tensor(seq[lo:hi], device=self.device)
+                p_t = torch.as_tensor(pos[lo:hi], device=self.device)
+                B.mla_append_cache(self.dims, h, hi - lo, s_t, p_t, self.w_dkv, self.w_kr, self.rope_cos,
+                                   self.rope_sin, self.rope_rows, self.cache.desc, ws, ws_bytes, self.stream)
 
     def fill_cache_direct(self, seed: int = 0):
         """Draw every cache row directly from the distribution the projection produces
@@ -165,14 +182,16 @@ class MLARunner:
         gen = torch.Generator(device=self.device)
         gen.manual_seed(2000 + 17 * self.w.seed + seed)
         rows = self.cache.rows
-        rows.copy_(torch.randn(rows.shape, generator=gen, device=self.device, dtype=torch.float32))
+        with self._on_own_stream():
+            rows.copy_(torch.randn(rows.shape, generator=gen, device=self.device, dtype=torch.float32))
 
     def draw_step_inputs(self, seed: int = 0):
         w = self.w
         gen = torch.Generator(device=self.device)
         gen.manual_seed(3000 + 17 * w.seed + seed)
-        for t in (self.h_new, self.q_nope, self.q_rope):
-            t.copy_(torch.randn(t.shape, generator=gen, device=self.device, dtype=torch.float32))
+        with self._on_own_stream():
+            for t in (self.h_new, self.q_nope, self.q_rope):
+                t.copy_(torch.randn(t.shape, generator=gen, device=self.device, dtype=torch.float32))
 
     # ------------------------------------------------------------------ the step
     def _on(self, stream):
@@ -363,6 +382,7 @@ class MLALayer(MLARunner):
         self.residual = torch.zeros((T, w.d_model), dtype=dt, device=dev)
         self.down = torch.empty((T, self.d_down), dtype=dt, device=dev)
         self.y = torch.empty((T, w.d_model), dtype=dt, device=dev)
+        torch.cuda.synchronize(dev)  # (as in MLARunner)
 
     def layer_step(self, stream=None):
         w, T, st = self.w, self.n_tok, self._on(stream)
