@@ -253,9 +253,10 @@ MLA_API mla_status mla_decode_attention_noalloc(const mla_dims* dims, const void
  *   scales [n_tok, ceil(width / 128)] fp32, dense, one per 128 values of a row (the last block may
  *          be shorter);  value = code * scale.
  *   s = amax / 448 and code = e4m3(x * (448 / amax)), each step rounded to fp32 and the code to
- *   nearest even, as the FP8 cache does; s = 1 for an all-zero block, and a block whose amax is
- *   below 2^-100 is coded against 2^-100.  A block that holds a NaN or an infinity stands for
- *   NaN.
+ *   nearest even; s = 1 for an all-zero block.  A block whose amax is below 2^-100 is coded against
+ *   2^-100, and a block that holds a NaN or an infinity stands for NaN.  (mla_append_cache writes the
+ *   same codes and scales but for these two: it leaves a NaN out of amax and codes it alone, and below
+ *   about 2^-119 its 448 / amax is infinite.)
  * Further conventions of these calls:
  *   - *_ld is the distance between consecutive rows in elements (bytes for codes), at least the
  *     row's width; elements between the width and *_ld are neither read nor written.
@@ -308,8 +309,8 @@ MLA_API mla_status mla_project_fp8(int32_t act_dtype, const uint8_t* x_codes, in
 /* mla_append_rows — append rows that are already projected: step 1 without its products, for
  * callers whose down projection is another kernel (mla_project_fp8, say).
  *   c = kv[t, :d_c], k = kv[t, d_c : d_c + d_rope]; with gamma, c is normed as in mla_norm_rows
- *   (over its d_c values); k is rotated by RoPE at pos[t]; the row is stored as in
- *   mla_append_cache (F32 / BF16 row, or E4M3 codes and scales plus the bf16 rope row).
+ *   (over its d_c values); k is rotated by RoPE at pos[t]; the row is stored where and in the layout
+ *   that mla_append_cache does (F32 / BF16 row, or the latent as an 8-bit row plus the bf16 rope row).
  *   kv:       [n_tok, d_c + d_rope] act, kv_ld elements between rows
  *   gamma:    [d_c] act, or NULL: the latent is stored as it is and eps is not used
  *   seq_idx, pos, rope_cos, rope_sin, rope_rows, cache: as in mla_append_cache, and so are the

@@ -26,8 +26,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // Scale and its reciprocal of a block whose largest magnitude is amax: amax / 448 and 448 / amax in
-// fp32 (the append's decision, so both write the same codes), 1 for an all-zero block.  Below
-// 2^-100 the block takes 2^-100's scale: 448 / amax would overflow under about 2^-119.
+// fp32, 1 for an all-zero block.  Between 2^-100 and the largest float that is mla_append_cache's decision, so both
+// write the same codes.  Below 2^-100 the block takes 2^-100's scale (448 / amax overflows under about 2^-119, as it
+// does there), and a NaN amax (max_nan) makes the block NaN, where that call's maximum leaves NaN out.
 __device__ __forceinline__ void block_scale(float amax, float& s, float& inv) {
   const float floor_ = 7.888609052210118e-31f;  // 2^-100
   const float a = amax < floor_ ? floor_ : amax;  // (a NaN stays)

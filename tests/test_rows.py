@@ -526,3 +526,48 @@ def test_tensors_on_no_or_another_device_are_refused(lib):
         lib.mla_quantize_rows(lib.MLA_F32, host, 64, 2, 64, x, 64, x)
     with pytest.raises(lib.MlaError):
         lib.mla_quantize_rows(lib.MLA_F32, x, 63, 2, 64, x, 64, x)
+
+
+def test_append_rows_codes_are_append_caches_codes(lib):
+    """8-bit cache, the same latents bit for bit (identity weights): the same codes and scales from both calls, for blocks
+    of zeros and of any size from 2^-100 up."""
+    lengths, d_c, d_rope = (5, 70), 512, 64
+    T, W = sum(lengths), d_c + d_rope
+    a, b = (Cache(lib, torch.bfloat16, "fp8", d_c, d_rope, 64, lengths) for _ in range(2))
+    size = torch.exp2(torch.linspace(-99, 99, T, device="cuda"))[:, None]
+    h = (randn((T, W), 12).clamp(-4, 4).sign() * (1 + randn((T, W), 13).abs().clamp(max=3)) * size).bfloat16()
+    h[3, :128] = 0
+    seq = torch.repeat_interleave(torch.arange(2), torch.tensor(lengths)).int().cuda()
+    pos = torch.cat([torch.arange(n) for n in lengths]).int().cuda()
+    cos, sin = rope_tables(lib, d_rope, 128)
+    eye = torch.eye(W, device="cuda").bfloat16()
+    dims = lib.mla_dims(W, d_c, d_rope, 64, 128, 4, 64, lib.MLA_BF16, lib.MLA_FP8_E4M3, 0.1)
+    n = lib.mla_append_workspace_size(dims, T)
+    ws = torch.empty(max(1, n), dtype=torch.uint8, device="cuda")
+    lib.mla_append_cache(dims, h, T, seq, pos, eye[:d_c].contiguous(), eye[d_c:].contiguous(), cos, sin, 128, a.desc, ws, n)
+    lib.mla_append_rows(b.dims, h, W, T, seq, pos, None, 0.0, cos, sin, 128, b.desc)
+    torch.cuda.synchronize()
+    assert lib.mla_check_device_error()[0] == 0
+    at = b.slots(seq, pos)
+    assert torch.equal(a.rows[at], b.rows[at]) and torch.equal(a.scales[at], b.scales[at])
+
+
+@pytest.mark.parametrize("d_rope", [64, 258])  # (the second goes by elements)
+def test_append_rows_tiny_and_nan_blocks(lib, d_rope):
+    """A latent block below 2^-100 is coded against 2^-100; one with a NaN or an infinity stands for NaN; the blocks
+    beside it are as ever."""
+    d_c, T = 256, 4
+    c = Cache(lib, torch.bfloat16, "fp8", d_c, d_rope, 64, (T,))
+    kv = randn((T, d_c + d_rope), 14).bfloat16()
+    kv[0, :128] = (1e-38 * randn((128,), 15)).bfloat16()
+    kv[0, 5] = 0
+    kv[1, 3], kv[2, 4] = float("nan"), float("inf")
+    seq, pos = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")
+    cos, sin = rope_tables(lib, d_rope, 64)
+    lib.mla_append_rows(c.dims, kv, d_c + d_rope, T, seq, pos, None, 0.0, cos, sin, 64, c.desc)
+    torch.cuda.synchronize()
+    assert lib.mla_check_device_error()[0] == 0
+    q, s, y = c.rows[c.slots(seq, pos)], c.scales[c.slots(seq, pos)], kv[:, :d_c].double()
+    assert torch.isnan(decoded(q, s, d_c)[1:3, :128]).all()
+    check_codes(q[[0, 3]], s[[0, 3]], y[[0, 3]], d_c, 2.0 ** -24)
+    check_codes(q[1:3, 128:].contiguous(), s[1:3, 1:], y[1:3, 128:], 128, 2.0 ** -24)
