@@ -571,3 +571,28 @@ def test_append_rows_tiny_and_nan_blocks(lib, d_rope):
     assert torch.isnan(decoded(q, s, d_c)[1:3, :128]).all()
     check_codes(q[[0, 3]], s[[0, 3]], y[[0, 3]], d_c, 2.0 ** -24)
     check_codes(q[1:3, 128:].contiguous(), s[1:3, 1:], y[1:3, 128:], 128, 2.0 ** -24)
+
+
+# a warp a row; a CTA a row; walking CTAs; a CTA a row of more values; streaming CTAs (bf16, f32); four chunks a thread; by
+# elements with a warp and with a CTA a row; rows read twice
+@pytest.mark.parametrize("act", ACT)
+@pytest.mark.parametrize("t,width", [(300, 512), (5, 1536), (2500, 1536), (40, 7168), (1300, 7168), (700, 16384), (3, 32768),
+                                     (700, 301), (601, 1501), (5, 8191), (2, 16385)])
+@pytest.mark.parametrize("sum_over", ["residual", "x"])
+def test_norm_in_place_everywhere(lib, act, t, width, sum_over):
+    """sum_out over the residual with y over x, and sum_out over x (with and without a residual), in every kernel."""
+    g = (1 + 0.1 * randn((width,), 3)).to(act)
+    for with_res in ((True,) if sum_over == "residual" else (True, False)):
+        x = randn((t, width), 1).to(act)
+        res = randn((t, width), 2).to(act) if with_res else None
+        r, want = norm_ref(x, res, g, 1e-5)
+        q = torch.empty((t, width), dtype=torch.uint8, device="cuda")
+        s = torch.empty((t, -(-width // 128)), device="cuda")
+        y = x if sum_over == "residual" else torch.empty_like(x)
+        total = res if sum_over == "residual" else x
+        lib.mla_norm_rows(dt(lib, act), x, width, res, width, g, t, width, 1e-5, total, width, y, width, q, width, s)
+        torch.cuda.synchronize()
+        near(total, r, 2.0 ** -24)
+        near(y, want)
+        check_codes(q, s, want, width)
+    assert lib.mla_check_device_error()[0] == 0
