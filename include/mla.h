@@ -273,7 +273,9 @@ MLA_API mla_status mla_decode_attention_noalloc(const mla_dims* dims, const void
 
 /* mla_norm_rows — root-mean-square norm with the residual's addition and an 8-bit output.
  *   r = x + residual,  y = r / sqrt(mean(r^2) + eps) * gamma
- * in fp32 from the unrounded sum r; each output is rounded once.
+ * in fp32 from the unrounded sum r; each output is rounded once.  (Squares are fp32 too: a row whose sum of
+ * squares passes its range gives y = 0, and with eps = 0 a row of zeros, or one whose squares all vanish,
+ * gives no finite y.)
  *   x:        [n_tok, width] act;  residual: [n_tok, width] act, or NULL (r = x)
  *   gamma:    [width] act, or NULL (a weight of 1)
  *   sum_out:  [n_tok, width] act, r rounded (the next residual), or NULL
@@ -316,7 +318,8 @@ MLA_API mla_status mla_project_fp8(int32_t act_dtype, const uint8_t* x_codes, in
  *   seq_idx, pos, rope_cos, rope_sin, rope_rows, cache: as in mla_append_cache, and so are the
  *   handling of bad sequence numbers, positions and page ids (the token is skipped and reported)
  *   and of two tokens with the same (sequence, position).  n_tok == 0 is a no-op.
- * Of dims the call uses d_c, d_rope, page_size, act_dtype and cache_dtype. */
+ * Of dims the call uses d_c, d_rope, page_size, act_dtype and cache_dtype; the others are checked as in
+ * every call. */
 MLA_API mla_status mla_append_rows(const mla_dims* dims, const void* kv, int64_t kv_ld, int32_t n_tok,
                            const int32_t* seq_idx, const int32_t* pos, const void* gamma, float eps,
                            const float* rope_cos, const float* rope_sin, int32_t rope_rows,

@@ -103,10 +103,11 @@ __global__ void __launch_bounds__(256) fp8_any_kernel(const Fp8Args a) {
 // copy each into a buffer of the owner's shared memory; the owner adds the S partial sums of its rows
 // in rank order and stores them: no workspace, no atomics.
 //
-// 64 x 7168 x 16384: 25.9 us, 4.5 TB/s of weights (their bytes at copy bandwidth: 18.2 us).  56 tiles split in two
-// leave 36 SMs idle, and the start, the exchange and the last sums take some 6 us; 64 x 18944 x 16384, which
-// fills the SMs, reads 5.9 TB/s.  64 x 2112 x 7168: 7.6 us, 1 x 576 x 2048: 3.2 us, the chain of wait, load, MMA,
-// exchange and store.  Tried: 8 promoting warps for 64 columns (42 us against 30 at the time), the exchange by
+// 64 x 7168 x 16384: 25.9 us in a burst, 28.5 in a loop of half a second; 4.5 TB/s of weights (their bytes at copy
+// bandwidth: 18.2 us).  56 tiles split in two leave 36 SMs idle (a tile is always 128 outputs high), and the start, the
+// exchange and the last sums take some 6 us; 64 x 18944 x 16384, which fills the SMs, reads 5.9 TB/s.
+// 64 x 2112 x 7168: 7.7 us (8.4 over 400 MB of operands), 1 x 576 x 2048: 3.1 us, the chain of wait, load, MMA, exchange and
+// store.  Tried: 8 promoting warps for 64 columns (42 us against 30 at the time), the exchange by
 // asynchronous 16-byte stores from registers (64 x 2112 x 7168 0.4 us longer than by bulk copies), the next
 // block's products loaded ahead of the sums (nothing: the issuing warp bound the blocks, not these).
 constexpr int A_BYTES = 128 * 128;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
 }
 
 // ------------------------------------------------------------------ many tokens
-// Bound by the tensor pipe.  A pair of CTAs (cta_group::2) computes 256 tokens x WN outputs: each CTA
+// Bound by the fp32 sums between the MMAs: the tensor pipe is active 55 % of the time.  A pair of CTAs (cta_group::2) computes 256 tokens x WN outputs: each CTA
 // loads 128 token rows and WN / 2 weight rows of a scale block, and the pair's MMA (M = 256, N = WN,
 // K = 32, four per block) leaves 128 tokens x WN outputs in each CTA's TMEM.  Here the tokens are the
 // lanes, so a thread scales its columns by one or two numbers per block, xs[t, b] ws[n / 128, b].  Eight
@@ -458,10 +459,12 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
 // ahead.  Persistent over tiles; a finished tile goes out through 4 KB of shared memory a warp and
 // TMA stores.
 //
-// 2048 x 7168 x 16384: 233 us, 2.06 PFLOP/s (a long loop of them runs at the power cap, 275 us).  A block of 160
-// outputs takes a pair 0.307 us, of 128 0.26; the MMAs alone need 0.215 for 128 outputs and 0.29 for 256 (an MMA
+// 2048 x 7168 x 16384: 232 us in a burst, 2.07 PFLOP/s (a long loop of them runs at the power cap, 278 us).  A block of
+// 160 outputs takes a pair 0.307 us, of 128 0.26; the MMAs alone need 0.215 for 128 outputs and 0.29 for 256 (an MMA
 // of N = 128 runs at two thirds of N = 256's rate).  What it waits for is the sums: 256 outputs leave TMEM room for two
-// accumulators only, and the tensor pipe idles while one is read (0.56 us a block); 192 outputs 0.42.
+// accumulators only, and the tensor pipe idles while one is read (0.56 us a block); 192 outputs 0.42.  That is some 580
+// clocks a block of 160 outputs, of which the packed FMAs of a scheduler's two promoting warps take about 160: the rest is
+// their chain of wait, TMEM load, wait and arrival.
 template <int WN>
 struct WdCfg {
   static constexpr int HC = WN / 2;                    // columns of a promoting warp

@@ -4,10 +4,12 @@
 //   quantise  s = max|y| / 448,  code = e4m3(y / s)  per 128 values        (mla_norm_rows, mla_quantize_rows)
 //   append    c' = norm(c) gamma, k' = RoPE_pos(k), into the paged cache   (mla_append_rows)
 //
-// All three are bound by HBM when there are many rows and by latency when there are few, so each
-// reads every input once into registers (16-byte loads, all of a thread's loads in flight before
-// the first use), reduces with shuffles, and writes every output once.  Sums and statistics are
-// fp32, nothing is rounded before it is stored.
+// All three are bound by HBM when there are many rows and by latency when there are few.  So the vector
+// kernels read every input once, with 16-byte loads into registers (all of a thread's loads in flight
+// before the first use) or, for many rows, by bulk copies into a ring in shared memory, reduce with
+// shuffles, and write every output once.  Of the kernels for other layouts, rows_any_kernel loads single
+// elements, once; rows_long_kernel reads x and the residual twice, append_rows_any_kernel a normed latent.  Sums
+// and statistics are fp32, nothing is rounded before it is stored.
 #include "mla_internal.cuh"
 #include "rows.cuh"
 #include "sm100_f8.cuh"
@@ -700,7 +702,8 @@ constexpr int AR_WARPS = 4;
 // position came one token earlier still) under way; a token a warp waited for each of these in turn.
 // With 16 lanes a warp's instructions serve two tokens, and these kernels issue for half of their time.
 // 40007 bf16 tokens of 512 + 64: 18.7 us, 5.5 TB/s (32 lanes 21.2; without the prefetch 25), into the
-// 8-bit cache 19.1 (22.8).
+// 8-bit cache 19.1 (22.8): a fifth fewer bytes in the same time, so instructions bound that form (the maxima over
+// 16 lanes, the scales by shuffles, the conversions).
 template <typename T, int LANES, int CH, bool FP8>
 __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const AppendParams p) {
   griddep_wait();
@@ -804,7 +807,8 @@ __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const Append
 }
 
 // Any d_c, d_rope, alignment and leading dimension: one warp per token, element accesses, the
-// latent part read twice when it is normed.  (No early start of the next grid, as in rows_long_kernel.)
+// latent part read twice when it is normed.  40007 tokens of 512 + 64 in rows of 577: bf16 31 us, float 41, into the
+// 8-bit cache 42 (vector kernel 19, 33, 19): bound by the number of 2- and 1-byte accesses.  (No early start of the next grid, as in rows_long_kernel.)
 template <typename T, bool FP8>
 __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_any_kernel(const AppendParams p) {
   griddep_wait();
@@ -938,6 +942,10 @@ static cudaError_t rows_impl(const RowsArgs& a, bool norm, cudaStream_t st) {
   //   up to 16384         a CTA per row, then     500 x 7168: 8.7 [streaming 9.9]
   //                       streaming CTAs          8191 x 7168: 87 [a CTA per row 129]; 3583 x 16384: 95 [132]
   //   up to 32768         a CTA per row
+  // Streaming needs room for two stages.  bf16 rows always have it; float rows with a residual and a staged weight up to
+  // 5632 values (two CTAs an SM) and from 8200 to 11264 (one), up to 7040 and 14080 without the weight's copy.  The
+  // others stay with a CTA per row: float, residual, sum and 8-bit rows out, 2048 x 11264 53.9 (5.6 TB/s), 2048 x 12288 70.5
+  // (4.6), whose kernel also spills (four chunks a thread in 64 registers).
   auto threads = [&](int ch) { return (unsigned)(((chunks + ch - 1) / ch + 31) / 32 * 32); };
   if (chunks <= 64)
     return launch_pdl(rows_warp_kernel<T, 2>, ((unsigned)a.n_tok + RW_WARPS - 1) / RW_WARPS, RW_WARPS * 32, st, 0, a);
