@@ -879,17 +879,19 @@ static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   return fn;
 }
 
-// 2-D map over bytes: boxes of 128 bytes x box_rows rows, 128-byte swizzle, zeros outside.
-static bool map_bytes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_rows) {
+// 2-D map over bytes: boxes of 128 bytes x box_rows rows, 128-byte swizzle, zeros outside.  kUnsupported: not a layout
+// that a map takes; anything else that goes wrong is an error of the driver's.
+static cudaError_t map_bytes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_rows) {
   auto enc = tmap_encoder();
-  if (!enc) return false;
+  if (!enc) return cudaErrorNotSupported;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {ld};
   cuuint32_t box[2] = {128, box_rows};
   cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : r == CUDA_ERROR_INVALID_VALUE ? kUnsupported : cudaErrorUnknown;
 }
 
 // What is looked up or set once per device: the few-token kernel's shared memory, and how many clusters
@@ -947,7 +949,9 @@ template <int BN, int OCC>
 static cudaError_t launch_skinny(const Fp8Args& a, int dev, int S, cudaStream_t st) {
   using C = p8::SkCfg<BN, OCC>;
   CUtensorMap mw, mx;
-  if (!map_bytes(&mw, a.w, a.K, a.N, a.K, 128) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN)) return kUnsupported;
+  cudaError_t e = map_bytes(&mw, a.w, a.K, a.N, a.K, 128);
+  if (e == cudaSuccess) e = map_bytes(&mx, a.x, a.K, a.T, a.x_ld, BN);
+  if (e != cudaSuccess) return e;
   const int blocks = (a.K + 127) / 128, tiles_n = (a.N + 127) / 128;
   const long tiles_t = (a.T + BN - 1) / BN;
   p8::SkParams p;
@@ -961,7 +965,7 @@ static cudaError_t launch_skinny(const Fp8Args& a, int dev, int S, cudaStream_t 
   p.out_ld = a.out_ld;
   p.out_f32 = a.act == MLA_F32;
   p.err = a.err;
-  cudaError_t e = skinny_ready<BN, OCC>(dev);
+  e = skinny_ready<BN, OCC>(dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, (unsigned)tiles_t);
@@ -1024,7 +1028,9 @@ template <int WN>
 static cudaError_t launch_wide(const Fp8Args& a, cudaStream_t st) {
   using C = p8::WdCfg<WN>;
   CUtensorMap mw, mx, mo;
-  if (!map_bytes(&mw, a.w, a.K, a.N, a.K, WN / 2) || !map_bytes(&mx, a.x, a.K, a.T, a.x_ld, 128)) return kUnsupported;
+  cudaError_t e = map_bytes(&mw, a.w, a.K, a.N, a.K, WN / 2);
+  if (e == cudaSuccess) e = map_bytes(&mx, a.x, a.K, a.T, a.x_ld, 128);
+  if (e != cudaSuccess) return e;
   p8::WdParams p;
   const bool tma_out = map_out(&mo, a);
   if (!tma_out) mo = mx;
@@ -1043,7 +1049,7 @@ static cudaError_t launch_wide(const Fp8Args& a, cudaStream_t st) {
   p.err = a.err;
   const long tiles = (long)p.tiles_t * p.tiles_n;
   if (tiles > (1 << 30)) return kUnsupported;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (tiles < 74 ? tiles : 74)));

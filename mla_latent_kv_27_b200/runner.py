@@ -5,7 +5,8 @@ latent cache, per-step inputs and outputs, workspaces; all allocated with torch)
 a decode step as four library calls on one stream:
 
     mla_append_cache     the step's new tokens -> cache            (step 1)
-    mla_absorb_query     q_lat = W_UK^T q_nope, q_rope rotated     (step 2)
+    mla_absorb_query     q_lat = W_UK^T q_nope, q_rope rotated     (step 2; its _early form,
+                         since the append in front does not write q_nope)
     mla_decode_attention split-KV attention + log-sum-exp combine  (steps 3, 4)
     mla_output_up        out = W_UV o_lat                          (step 5)
 
