@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(SkCfg<BN, OCC>::THREADS, OCC)
 }
 
 // ------------------------------------------------------------------ many tokens
-// Bound by the fp32 sums between the MMAs: the tensor pipe is active 52 to 55 % of the time.  A pair of CTAs (cta_group::2) computes 256 tokens x WN outputs: each CTA
+// Bound by the fp32 sums between the MMAs: the tensor pipe is active 52 to 55 % of the time.  A pair of CTAs
+// (cta_group::2) computes 256 tokens x WN outputs: each CTA
 // loads 128 token rows and WN / 2 weight rows of a scale block, and the pair's MMA (M = 256, N = WN,
 // K = 32, four per block) leaves 128 tokens x WN outputs in each CTA's TMEM.  Here the tokens are the
 // lanes, so a thread scales its columns by one or two numbers per block, xs[t, b] ws[n / 128, b].  Eight

@@ -808,7 +808,8 @@ __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_kernel(const Append
 
 // Any d_c, d_rope, alignment and leading dimension: one warp per token, element accesses, the
 // latent part read twice when it is normed.  40007 tokens of 512 + 64 in rows of 577: bf16 31 us, float 41, into the
-// 8-bit cache 42 (vector kernel 19, 33, 19): bound by the number of 2- and 1-byte accesses.  (No early start of the next grid, as in rows_long_kernel.)
+// 8-bit cache 42 (vector kernel 19, 33, 19): bound by the number of 2- and 1-byte accesses.  (No early start of the
+// next grid, as in rows_long_kernel.)
 template <typename T, bool FP8>
 __global__ void __launch_bounds__(AR_WARPS * 32) append_rows_any_kernel(const AppendParams p) {
   griddep_wait();
